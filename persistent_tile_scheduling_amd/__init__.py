@@ -369,3 +369,11 @@ def gemm(a: torch.Tensor, b: torch.Tensor, out_dtype=torch.float32, schedule="st
     with Plan([(m, n, kk, lda, ldb, ldd)], out.dtype, tile, schedule, num_workers) as p:
         p.run([(a, b, out)])
     return out
+
+
+# The routed-experts operators share the helpers above, so they come last.
+from .experts import (MoeRouting, PTS_FP8_BLOCK, PTS_MOE_MAX_EXPERTS, PTS_MOE_MAX_GROUPS,  # noqa: E402, F401
+                      PTS_MOE_MAX_TOP, PTS_SCORE_SIGMOID, PTS_SCORE_SOFTMAX, gemm_fp8, gemm_fp8_experts, moe_combine,
+                      moe_combine_backward, moe_fp8, moe_route, moe_route_backward, pts_gemm_fp8,
+                      pts_gemm_fp8_experts, pts_moe_combine, pts_moe_combine_backward, pts_moe_route,
+                      pts_moe_route_backward, pts_moe_route_workspace, pts_quantize_fp8, quantize_fp8)

@@ -12,10 +12,11 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+CSRC_EXPERTS = os.path.join(HERE, "csrc_experts")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libpts_gemm.so")
-SOURCES = [os.path.join(CSRC, "pts_gemm.hip")]
+SOURCES = [os.path.join(CSRC, "pts_gemm.hip"), os.path.join(CSRC_EXPERTS, "pts_experts.hip")]
 ARCH = os.environ.get("PTS_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
@@ -40,7 +41,7 @@ def hipcc() -> str:
 def build(out: str = LIB, extra: list[str] | None = None, verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(out), exist_ok=True)
     tmp = out + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra or []), f"-I{INCLUDE}", f"-I{CSRC}", *SOURCES, "-o", tmp]
+    cmd = [hipcc(), *HIPCC_FLAGS, *(extra or []), f"-I{INCLUDE}", f"-I{CSRC}", f"-I{CSRC_EXPERTS}", *SOURCES, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,11 +60,12 @@ def sources_newer_than(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    for d, _, files in os.walk(CSRC):
-        for f in files:
-            if os.path.getmtime(os.path.join(d, f)) > t:
-                return True
-    return os.path.getmtime(os.path.join(INCLUDE, "pts_gemm.h")) > t
+    for top in (CSRC, CSRC_EXPERTS, INCLUDE):
+        for d, _, files in os.walk(top):
+            for f in files:
+                if os.path.getmtime(os.path.join(d, f)) > t:
+                    return True
+    return False
 
 
 if __name__ == "__main__":

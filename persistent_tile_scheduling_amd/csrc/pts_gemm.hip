@@ -16,12 +16,13 @@
 
 #include "device/aux_kernels.h"
 #include "device/gemm_kernel.h"
+#include "host_error.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-gemm_status fail(gemm_status s, const char *fmt, ...)
+gemm_status pts::fail(gemm_status s, const char *fmt, ...)
 {
     char buf[512];
     va_list ap;
@@ -32,10 +33,15 @@ gemm_status fail(gemm_status s, const char *fmt, ...)
     return s;
 }
 
-gemm_status hip_fail(hipError_t e, const char *what)
+gemm_status pts::hip_fail(hipError_t e, const char *what)
 {
     return fail(GEMM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+namespace {
+
+using pts::fail;
+using pts::hip_fail;
 
 // One compiled kernel configuration.
 struct KernelEntry {

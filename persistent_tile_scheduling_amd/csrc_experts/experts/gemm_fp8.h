@@ -1,0 +1,565 @@
+// Products of e4m3 matrices with an fp32 scale per block of 128:
+//
+//   D[i][j] = sum_b sa[i][b] sb[j or j / 128][b] sum_{k in block b} A[i][k] B[k][j]
+//
+// one dense product, or one per expert over rows ordered by expert. The inner
+// sum of a block starts from zero in the matrix unit; the outer sum is an fp32
+// multiply-add of its result by the block's scale. The blocks are summed in
+// ascending order, one accumulator per output, so a result does not depend on
+// timing.
+//
+// Operand bytes per k block and row are 128, as in a 64-deep bf16 tile.
+#pragma once
+
+#include "device/common.h"
+#include "device/scheduler.h"
+
+namespace pts {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+struct Fp8Args {
+    const uint8_t *a, *b;
+    const float *sa, *sb;
+    void *d;
+    const int32_t *offsets; // experts + 1 row offsets, or null: one dense product
+    const int32_t *rows;    // row of A of each row of D, or null: the same row
+    int64_t lda, ldb, ldd;  // elements
+    int64_t sa_m, sa_k, sb_n, sb_k; // element strides of the scales
+    int64_t b_expert, sb_expert;    // element strides from one expert's B to the next
+    int32_t m, n, k, nk;
+    int32_t tiles_n, experts, a_rows;
+    int32_t d_vec; // D's rows are 16-byte aligned
+};
+
+// One row's share of a k block in a lane: lane l has, of row l % 16, the two
+// 16-byte chunks l / 16 and l / 16 + 4 (which chunk is which k does not matter
+// as long as both operands agree), as e4m3 or widened to bf16.
+//
+// The matrix unit sums e4m3 products in groups of 8 consecutive k: within a
+// group, what lies 14 or more binary places below the largest product's
+// exponent is dropped before the fp32 addition (found by adding a single small
+// product to a large one; the same for the 16 x 16 x 32 form). On normal data
+// that is 1.4e-5 of the result, far below bf16's 2^-8, but not fp32. So bf16
+// results are computed from e4m3 products, one v_mfma_f32_16x16x128_f8f6f4 per
+// 16 x 16 outputs and k block, at twice bf16's rate; and fp32 results (EXACT)
+// from the same codes widened to bf16, whose products the unit sums in fp32,
+// four v_mfma_f32_16x16x32_bf16 per block.
+template <bool EXACT> struct Fragment;
+template <> struct Fragment<false> {
+    i32x8 v;
+    __device__ __forceinline__ void set(i32x4 lo, i32x4 hi) { v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+};
+template <> struct Fragment<true> {
+    bf16x8 v[4];
+    __device__ __forceinline__ void set(i32x4 lo, i32x4 hi)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const i32x4 src = i < 2 ? lo : hi;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t word = (uint32_t)src[(i & 1) * 2 + w];
+                const bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, 1.0f, false);
+                const bf16x2 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, 1.0f, true);
+                v[i][4 * w] = x[0];
+                v[i][4 * w + 1] = x[1];
+                v[i][4 * w + 2] = y[0];
+                v[i][4 * w + 3] = y[1];
+            }
+        }
+    }
+};
+
+// The sums of one k block for 16 rows of X against 16 rows of Y: lane l gets
+// rows 4 (l / 16) .. + 3 of X against row l % 16 of Y.
+__device__ __forceinline__ f32x4 block_sums(const Fragment<false> &x, const Fragment<false> &y)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 block_sums(const Fragment<true> &x, const Fragment<true> &y)
+{
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.v[i], y.v[i], c, 0, 0, 0);
+    return c;
+}
+
+// One output tile: rows [row0, row0 + vm) of D and columns [col0, col0 + vn).
+struct Fp8Tile {
+    int expert, row0, vm, col0, vn;
+};
+
+// Position inside one problem: groups of 8 tile rows walked column by column,
+// so that 32 consecutive positions (one die's share of a round) are an 8 x 4
+// block whose operands its L2 holds.
+__device__ __forceinline__ void fp8_raster(int local, int tiles_m, int tiles_n, int &tm, int &tn)
+{
+    const int first = local / (8 * tiles_n) * 8;
+    const int in = local - first * tiles_n;
+    const int rows = min(8, tiles_m - first);
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+// The tile at position t: the expert is found by a scan of the experts' tile
+// counts, 64 at a time, one per lane. Offsets are clamped into [0, m] and to be
+// non-decreasing, so a bad table cannot lead outside the operands. Returns
+// false past the last tile.
+__device__ __forceinline__ bool fp8_find_tile(const Fp8Args &args, int bm, int bn, int t, Fp8Tile &tile)
+{
+    if (args.offsets == nullptr) {
+        const int tiles_m = (args.m + bm - 1) / bm;
+        if (t >= tiles_m * args.tiles_n)
+            return false;
+        int tm, tn;
+        fp8_raster(t, tiles_m, args.tiles_n, tm, tn);
+        tile.expert = 0;
+        tile.row0 = tm * bm;
+        tile.vm = min(bm, args.m - tile.row0);
+        tile.col0 = tn * bn;
+        tile.vn = min(bn, args.n - tile.col0);
+        return true;
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int e0 = 0; e0 < args.experts; e0 += 64) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < args.experts) {
+            lo = min(max(args.offsets[e], 0), args.m);
+            hi = min(max(args.offsets[e + 1], lo), args.m);
+        }
+        const int tiles = (hi - lo + bm - 1) / bm * args.tiles_n;
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(sum, d);
+            if (lane >= d)
+                sum += v;
+        }
+        const uint64_t past = __ballot(before + sum > t);
+        if (past != 0) {
+            const int src = __builtin_ctzll(past);
+            const int begin = __builtin_amdgcn_readlane(sum - tiles, src) + before;
+            const int elo = __builtin_amdgcn_readlane(lo, src), ehi = __builtin_amdgcn_readlane(hi, src);
+            int tm, tn;
+            fp8_raster(t - begin, (ehi - elo + bm - 1) / bm, args.tiles_n, tm, tn);
+            tile.expert = e0 + src;
+            tile.row0 = elo + tm * bm;
+            tile.vm = min(bm, ehi - tile.row0);
+            tile.col0 = tn * bn;
+            tile.vn = min(bn, args.n - tile.col0);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
+// Upper bound of fp8_find_tile's positions is not known on the host for
+// experts: a worker needs the total to deal positions to the dies.
+__device__ __forceinline__ int fp8_total_tiles(const Fp8Args &args, int bm)
+{
+    if (args.offsets == nullptr)
+        return (args.m + bm - 1) / bm * args.tiles_n;
+    const int lane = threadIdx.x & 63;
+    int tiles = 0;
+    for (int e = lane; e < args.experts; e += 64) {
+        const int lo = min(max(args.offsets[e], 0), args.m);
+        const int hi = min(max(args.offsets[e + 1], lo), args.m);
+        tiles += (hi - lo + bm - 1) / bm;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2)
+        tiles += __shfl_xor(tiles, d);
+    return uniform(tiles) * args.tiles_n;
+}
+
+// Row of A that row p of D reads.
+__device__ __forceinline__ int fp8_a_row(const Fp8Args &args, int p)
+{
+    if (args.rows == nullptr)
+        return p;
+    return min(max(args.rows[p], 0), args.a_rows - 1);
+}
+
+// N consecutive values of one row of D, of which the first `valid` exist.
+template <bool BF16, int N>
+__device__ __forceinline__ void fp8_store_row(void *d, int64_t at, const float (&v)[N], int valid, bool vec)
+{
+    constexpr int W = BF16 ? 8 : 4; // elements per 16 bytes
+#pragma unroll
+    for (int c = 0; c < N; c += W) {
+        if (vec && c + W <= valid) {
+            u32x4 w;
+            if constexpr (BF16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bf16x2 h = {(__bf16)v[c + 2 * i], (__bf16)v[c + 2 * i + 1]};
+                    w[i] = __builtin_bit_cast(uint32_t, h);
+                }
+                __builtin_nontemporal_store(w, (u32x4 *)((uint16_t *)d + at + c));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = __float_as_uint(v[c + i]);
+                __builtin_nontemporal_store(w, (u32x4 *)((float *)d + at + c));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (c + i < valid) {
+                    if constexpr (BF16)
+                        ((__bf16 *)d)[at + c + i] = (__bf16)v[c + i];
+                    else
+                        ((float *)d)[at + c + i] = v[c + i];
+                }
+        }
+    }
+}
+
+// ---- tiles through LDS -------------------------------------------------------
+
+// WM_ x WN_ waves, each a (BM / WM_) x (BN / WN_) piece. ROWS: B's scales are
+// per row of 128 k (as A's), otherwise per 128 x 128.
+template <int BM_, int BN_, int WM_, int WN_, bool ROWS_, bool BF16_>
+struct Fp8Config {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr bool ROWS = ROWS_, BF16 = BF16_, EXACT = !BF16_;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, MI = WTM / 16, NI = WTN / 16;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    static constexpr int S_BYTES = (BM + BN) * 4;
+    static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
+    static constexpr int LOADS_A = A_BYTES / 16 / THREADS, LOADS_B = B_BYTES / 16 / THREADS;
+    static_assert(BM + BN <= THREADS && BM % 64 == 0 && BN % 64 == 0, "one scale per thread and stage");
+    static_assert(NI == 4 && 128 % WTN == 0, "a wave's columns share a block scale, 16 per lane");
+    static_assert(2 * STAGE <= 160 * 1024, "two stages");
+};
+
+template <class C>
+struct Fp8Loop {
+    // A's rows and B's columns keep their 128 bytes of a k block in eight
+    // 16-byte chunks, chunk c at position c ^ swizzle(row), so that a wave-wide
+    // fragment read covers every bank once. A fragment holds 16 consecutive
+    // rows of A, but of B the columns 16 j + 4 ni + t (j, t = 0..3): a lane
+    // then owns 16 consecutive columns of D over its four blocks, which it
+    // stores as whole 16-byte pieces straight from its registers.
+    static __device__ __forceinline__ int swizzle_a(int r) { return (r >> 1) & 7; }
+    static __device__ __forceinline__ int swizzle_b(int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); }
+
+    u32x4 a_rsrc, b_rsrc, s_rsrc;
+    uint32_t a_off[C::LOADS_A], b_off[C::LOADS_B], s_off;
+    uint32_t s_step; // bytes from one k block's scales to the next
+    int wave;
+
+    __device__ __forceinline__ void setup(const Fp8Args &args, const Fp8Tile &t, int tid)
+    {
+        const int lane = tid & 63;
+        wave = uniform(tid >> 6);
+        const int64_t first = args.rows == nullptr ? t.row0 : 0;
+        a_rsrc = buffer_rsrc(args.a + first * args.lda);
+        b_rsrc = buffer_rsrc(args.b + t.expert * args.b_expert + (int64_t)t.col0 * args.ldb);
+#pragma unroll
+        for (int i = 0; i < C::LOADS_A; ++i) {
+            const int r = (wave * C::LOADS_A + i) * 8 + lane / 8;
+            const int row = fp8_a_row(args, t.row0 + min(r, t.vm - 1)) - (int)first;
+            a_off[i] = (uint32_t)row * (uint32_t)args.lda + (((lane & 7) ^ swizzle_a(r)) << 4);
+        }
+#pragma unroll
+        for (int i = 0; i < C::LOADS_B; ++i) {
+            const int r = (wave * C::LOADS_B + i) * 8 + lane / 8;
+            b_off[i] = (uint32_t)min(r, t.vn - 1) * (uint32_t)args.ldb + (((lane & 7) ^ swizzle_b(r)) << 4);
+        }
+        s_off = s_step = 0;
+        s_rsrc = a_rsrc;
+        if (wave * 64 < C::BM) {
+            const int row = fp8_a_row(args, t.row0 + min(wave * 64 + lane, t.vm - 1)) - (int)first;
+            s_rsrc = buffer_rsrc(args.sa + first * args.sa_m);
+            s_off = (uint32_t)row * (uint32_t)args.sa_m * 4u;
+            s_step = (uint32_t)args.sa_k * 4u;
+        } else if (wave * 64 < C::BM + C::BN) {
+            const int col = t.col0 + min(wave * 64 + lane - C::BM, t.vn - 1);
+            s_rsrc = buffer_rsrc(args.sb + t.expert * args.sb_expert);
+            s_off = (uint32_t)(C::ROWS ? col : col >> 7) * (uint32_t)args.sb_n * 4u;
+            s_step = (uint32_t)args.sb_k * 4u;
+        }
+    }
+
+    // Start the loads of k block kb into the stage at LDS address `stage`.
+    // In the last, partial block a chunk past the row's end reads the last
+    // chunk instead (cleared before it is used).
+    __device__ __forceinline__ void issue(uint32_t stage, int kb, int k)
+    {
+        const uint32_t at = (uint32_t)kb * 128u;
+        const int left = k - kb * 128;
+        if (left >= 128) {
+#pragma unroll
+            for (int i = 0; i < C::LOADS_A; ++i)
+                dma_load16_imm(stage + wave * (C::LOADS_A * 1024), i * 1024, a_off[i], a_rsrc, at);
+#pragma unroll
+            for (int i = 0; i < C::LOADS_B; ++i)
+                dma_load16_imm(stage + wave * (C::LOADS_B * 1024), C::A_BYTES + i * 1024, b_off[i], b_rsrc, at);
+        } else {
+            const uint32_t last = (uint32_t)((left - 1) / 16);
+            const uint32_t lane = lane_id();
+#pragma unroll
+            for (int i = 0; i < C::LOADS_A; ++i) {
+                const int r = (wave * C::LOADS_A + i) * 8 + (int)lane / 8;
+                const uint32_t c = (lane & 7) ^ swizzle_a(r);
+                dma_load16_imm(stage + wave * (C::LOADS_A * 1024), i * 1024,
+                               a_off[i] - ((c > last ? c - last : 0u) << 4), a_rsrc, at);
+            }
+#pragma unroll
+            for (int i = 0; i < C::LOADS_B; ++i) {
+                const int r = (wave * C::LOADS_B + i) * 8 + (int)lane / 8;
+                const uint32_t c = (lane & 7) ^ swizzle_b(r);
+                dma_load16_imm(stage + wave * (C::LOADS_B * 1024), C::A_BYTES + i * 1024,
+                               b_off[i] - ((c > last ? c - last : 0u) << 4), b_rsrc, at);
+            }
+        }
+        if (C::BM + C::BN == C::THREADS || wave * 64 < C::BM + C::BN)
+            dma_load4(stage + C::A_BYTES + C::B_BYTES + wave * 256, s_off, s_rsrc, (uint32_t)kb * s_step);
+    }
+
+    // One wave-wide 4-byte-per-lane global -> LDS load (see dma_load16).
+    static __device__ __forceinline__ void dma_load4(uint32_t lds_addr, uint32_t voff, u32x4 rsrc, uint32_t soff)
+    {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                     :
+                     : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
+                     : "memory");
+    }
+
+    // Clear the bytes past the row's end in a partial k block of `left` bytes.
+    static __device__ __forceinline__ void clear_tail(uint8_t *stage, int left, int tid)
+    {
+        const int c0 = left / 16;
+        for (int i = tid; i < (C::BM + C::BN) * 8; i += C::THREADS) {
+            const int r = i / 8, c = i % 8;
+            if (c < c0)
+                continue;
+            const int swz = r < C::BM ? swizzle_a(r) : swizzle_b(r - C::BM);
+            u32x4 *p = (u32x4 *)(stage + r * 128 + ((c ^ swz) << 4));
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (c == c0 && left % 16 != 0) {
+                v = *p;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int bytes = min(max(left - c0 * 16 - 4 * w, 0), 4);
+                    v[w] = bytes == 4 ? v[w] : v[w] & ((1u << (8 * bytes)) - 1u);
+                }
+            }
+            *p = v;
+        }
+    }
+};
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8Args args)
+{
+    using Loop = Fp8Loop<C>;
+    __shared__ __align__(1024) uint8_t smem[2 * C::STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int l16 = lane & 15, g = lane >> 4;
+    const int a_at = (wm * C::WTM + l16) * 128 + ((g ^ Loop::swizzle_a(l16)) << 4);
+    const int b_row = wn * C::WTN + (l16 >> 2) * 16 + (l16 & 3);
+    const int b_at = C::A_BYTES + b_row * 128 + ((g ^ Loop::swizzle_b(b_row)) << 4);
+    const int total = fp8_total_tiles(args, C::BM);
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        Fp8Tile tile;
+        if (!fp8_find_tile(args, C::BM, C::BN, static_position(t, total, gridDim.x), tile))
+            break;
+        Loop loop;
+        loop.setup(args, tile, tid);
+        f32x4 acc[C::MI][C::NI];
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j)
+                acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        barrier_lds(); // every wave has read the last tile's stages
+        const uint32_t lds = lds_address(smem);
+        if (args.nk > 0)
+            loop.issue(lds, 0, args.k);
+        for (int kb = 0; kb < args.nk; ++kb) {
+            uint8_t *stage = smem + (kb & 1) * C::STAGE;
+            wait_vmcnt<0>();
+            barrier_lds(); // this stage has landed for every wave, and every wave has read the other
+            if (args.k - kb * 128 < 128) {
+                Loop::clear_tail(stage, args.k - kb * 128, tid);
+                barrier_lds();
+            }
+            if (kb + 1 < args.nk)
+                loop.issue(lds + ((kb + 1) & 1) * C::STAGE, kb + 1, args.k);
+            const float *sa = (const float *)(stage + C::A_BYTES + C::B_BYTES) + wm * C::WTM + l16;
+            const float *sb = (const float *)(stage + C::A_BYTES + C::B_BYTES) + C::BM + wn * C::WTN;
+            Fragment<C::EXACT> b[C::NI];
+            f32x4 col[C::NI];
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j) {
+                const i32x4 lo = *(const i32x4 *)(stage + b_at + j * 512);
+                const i32x4 hi = *(const i32x4 *)(stage + (b_at ^ 64) + j * 512);
+                b[j].set(lo, hi);
+                if constexpr (C::ROWS)
+                    col[j] = *(const f32x4 *)(sb + g * 16 + j * 4);
+            }
+            const float block = C::ROWS ? 1.0f : sb[0];
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i) {
+                const i32x4 lo = *(const i32x4 *)(stage + a_at + i * 2048);
+                const i32x4 hi = *(const i32x4 *)(stage + (a_at ^ 64) + i * 2048);
+                Fragment<C::EXACT> a;
+                a.set(lo, hi);
+                const float s = sa[i * 16] * block;
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j) {
+                    const f32x4 p = block_sums(b[j], a);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][r] = fmaf(p[r], C::ROWS ? s * col[j][r] : s, acc[i][j][r]);
+                }
+            }
+        }
+        const int col0 = wn * C::WTN + g * 16;
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i) {
+            const int row = wm * C::WTM + i * 16 + l16;
+            if (row < tile.vm && col0 < tile.vn) {
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[j * 4 + r] = acc[i][j][r];
+                fp8_store_row<C::BF16, 16>(args.d, (int64_t)(tile.row0 + row) * args.ldd + tile.col0 + col0, v,
+                                           tile.vn - col0, args.d_vec);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ i32x4 half(i32x8 v, int h) { return h ? i32x4{v[4], v[5], v[6], v[7]} : i32x4{v[0], v[1], v[2], v[3]}; }
+
+// ---- few rows ----------------------------------------------------------------
+
+// Up to 16 MB rows against 16 columns per workgroup, straight from memory to
+// registers: with so few rows every byte of B is used by one workgroup only, so
+// LDS would add a hop and a barrier. The eight waves take the k blocks in turn
+// (wave w: w, w + 8, ...), which gives 4096-deep weights eight independent
+// streams of loads per column strip, and their partial sums are added in wave
+// order through LDS at the end. Memory bound, so the codes are always widened.
+template <int MB, bool ROWS, bool BF16>
+__global__ __launch_bounds__(512) void gemm_fp8_rows_kernel(const Fp8Args args)
+{
+    constexpr int WAVES = 8, UNROLL = MB == 1 ? 4 : 2;
+    __shared__ __align__(16) float part[WAVES][MB * 16][16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    Fp8Tile tile;
+    if (!fp8_find_tile(args, MB * 16, 16, blockIdx.x, tile))
+        return;
+    const uint8_t *ap[MB];
+    const float *sap[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int row = fp8_a_row(args, tile.row0 + min(i * 16 + l16, tile.vm - 1));
+        ap[i] = args.a + (int64_t)row * args.lda;
+        sap[i] = args.sa + (int64_t)row * args.sa_m;
+    }
+    const uint8_t *bp = args.b + tile.expert * args.b_expert + (int64_t)(tile.col0 + min(l16, tile.vn - 1)) * args.ldb;
+    const float *sbp = args.sb + tile.expert * args.sb_expert;
+    const int c4 = tile.col0 + g * 4; // the four columns this lane's results belong to
+    f32x4 acc[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = wave; k0 < args.nk; k0 += WAVES * UNROLL) {
+        i32x8 b[UNROLL], a[UNROLL][MB];
+        float sa[UNROLL][MB];
+        f32x4 sb[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int kb = min(k0 + u * WAVES, args.nk - 1); // past the end: read again, not used
+            const int last = min(7, (args.k - kb * 128 - 1) / 16);
+            const int64_t lo = (int64_t)kb * 128 + min(g, last) * 16, hi = (int64_t)kb * 128 + min(g + 4, last) * 16;
+            b[u] = __builtin_shufflevector(*(const i32x4 *)(bp + lo), *(const i32x4 *)(bp + hi), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                a[u][i] = __builtin_shufflevector(*(const i32x4 *)(ap[i] + lo), *(const i32x4 *)(ap[i] + hi), 0, 1, 2, 3,
+                                                  4, 5, 6, 7);
+                sa[u][i] = sap[i][kb * args.sa_k];
+            }
+            if constexpr (ROWS) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sb[u][r] = sbp[min(c4 + r, args.n - 1) * args.sb_n + kb * args.sb_k];
+            } else {
+                const float s = sbp[(tile.col0 >> 7) * args.sb_n + kb * args.sb_k];
+                sb[u] = f32x4{s, s, s, s};
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int kb = k0 + u * WAVES;
+            if (kb >= args.nk)
+                break;
+            const int left = args.k - kb * 128;
+            if (left < 128) { // bytes past the end of the rows are cleared in both operands
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const int at = (w < 4 ? g : g + 4) * 16 + (w & 3) * 4;
+                    const int bytes = min(max(left - at, 0), 4);
+                    const int mask = bytes == 4 ? -1 : (int)((1u << (8 * bytes)) - 1u);
+                    b[u][w] &= mask;
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+                        a[u][i][w] &= mask;
+                }
+            }
+            Fragment<true> x;
+            x.set(half(b[u], 0), half(b[u], 1));
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                Fragment<true> y;
+                y.set(half(a[u][i], 0), half(a[u][i], 1));
+                const f32x4 p = block_sums(x, y);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[i][r] = fmaf(p[r], sa[u][i] * sb[u][r], acc[i][r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        *(f32x4 *)&part[wave][i * 16 + l16][g * 4] = acc[i];
+    __syncthreads();
+    if (tid < MB * 64) {
+        const int r = tid >> 2, c = (tid & 3) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const f32x4 p = *(const f32x4 *)&part[w][r][c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] += p[i];
+        }
+        if (r < tile.vm)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i < tile.vn) {
+                    const int64_t at = (int64_t)(tile.row0 + r) * args.ldd + tile.col0 + c + i;
+                    if constexpr (BF16)
+                        ((__bf16 *)args.d)[at] = (__bf16)v[i];
+                    else
+                        ((float *)args.d)[at] = v[i];
+                }
+    }
+}
+
+} // namespace pts
