@@ -288,9 +288,9 @@ struct Fp8Loop {
         }
     }
 
-    // Start the loads of k block kb into the stage at LDS address `stage`.
-    // In the last, partial block a chunk past the row's end reads the last
-    // chunk instead (cleared before it is used).
+    // Start the loads of k block kb into the stage at LDS address `stage`, all
+    // at once. In the last, partial block a chunk past the row's end reads the
+    // last chunk instead (cleared before it is used).
     __device__ __forceinline__ void issue(uint32_t stage, int kb, int k)
     {
         const uint32_t at = (uint32_t)kb * 128u;
@@ -321,6 +321,20 @@ struct Fp8Loop {
             }
         }
         if (C::BM + C::BN == C::THREADS || wave * 64 < C::BM + C::BN)
+            dma_load4(stage + C::A_BYTES + C::B_BYTES + wave * 256, s_off, s_rsrc, (uint32_t)kb * s_step);
+    }
+
+    // Load I of the PIECES that `issue` starts, for a whole k block.
+    static constexpr int PIECES = C::LOADS_A + C::LOADS_B + 1;
+    template <int I> __device__ __forceinline__ void issue_piece(uint32_t stage, int kb)
+    {
+        const uint32_t at = (uint32_t)kb * 128u;
+        if constexpr (I < C::LOADS_A)
+            dma_load16_imm(stage + wave * (C::LOADS_A * 1024), I * 1024, a_off[I], a_rsrc, at);
+        else if constexpr (I < C::LOADS_A + C::LOADS_B)
+            dma_load16_imm(stage + wave * (C::LOADS_B * 1024), C::A_BYTES + (I - C::LOADS_A) * 1024, b_off[I - C::LOADS_A],
+                           b_rsrc, at);
+        else if (C::BM + C::BN == C::THREADS || wave * 64 < C::BM + C::BN)
             dma_load4(stage + C::A_BYTES + C::B_BYTES + wave * 256, s_off, s_rsrc, (uint32_t)kb * s_step);
     }
 
@@ -357,85 +371,239 @@ struct Fp8Loop {
     }
 };
 
+enum : int { LAST = 0, GENERAL = 1, STEADY = 2 }; // kinds of k block
+
+// Fix the order of what stands before and after in the instruction stream.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// One wave's share of the tile: its fragments of the two operands and scales
+// for the k block being computed, and the sums not yet added up.
+template <class C> struct Fp8Wave {
+    static constexpr int MI = C::MI, NI = C::NI;
+    // Blocks of a k block in the order of their matrix instructions, STEP at a
+    // time: EXACT interleaves two, whose four instructions each depend on the
+    // one before. The scaled sum of a step is added LAG steps later, so that
+    // the multiply-adds run under the matrix instructions that follow.
+    static constexpr int STEP = C::EXACT ? 2 : 1, STEPS = MI * NI / STEP, LAG = C::EXACT ? 1 : 2, RING = 2 * LAG;
+    f32x4 acc[MI][NI], sums[RING][STEP];
+    Fragment<C::EXACT> a[2], b[NI];
+    f32x4 col[NI]; // ROWS: the scales of this lane's columns
+    float scale[MI], late; // row scales of this k block; the last row's of the one before
+    int at_a, at_b, at_sa, at_sb; // this lane's places in stage 0, byte offsets
+
+    __device__ __forceinline__ void init(int wm, int wn, int lane)
+    {
+        const int l16 = lane & 15, g = lane >> 4;
+        const int b_row = wn * C::WTN + (l16 >> 2) * 16 + (l16 & 3);
+        at_a = (wm * C::WTM + l16) * 128 + ((g ^ Fp8Loop<C>::swizzle_a(l16)) << 4);
+        at_b = C::A_BYTES + b_row * 128 + ((g ^ Fp8Loop<C>::swizzle_b(b_row)) << 4);
+        at_sa = C::A_BYTES + C::B_BYTES + (wm * C::WTM + l16) * 4;
+        at_sb = C::A_BYTES + C::B_BYTES + (C::BM + wn * C::WTN + (C::ROWS ? g * 16 : 0)) * 4;
+    }
+    __device__ __forceinline__ void start_tile()
+    {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < RING; ++i)
+#pragma unroll
+            for (int j = 0; j < STEP; ++j)
+                sums[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            col[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        late = 0.f;
+        scale[MI - 1] = 0.f;
+    }
+    // `stage`: its first byte in LDS.
+    __device__ __forceinline__ void load_a(int which, int i, const uint8_t *stage)
+    {
+        a[which].set(*(const i32x4 *)(stage + at_a + i * 2048), *(const i32x4 *)(stage + (at_a ^ 64) + i * 2048));
+    }
+    __device__ __forceinline__ void load_b(int j, const uint8_t *stage)
+    {
+        b[j].set(*(const i32x4 *)(stage + at_b + j * 512), *(const i32x4 *)(stage + (at_b ^ 64) + j * 512));
+    }
+    // The new row scales; the old last row's stays for the sums in flight.
+    __device__ __forceinline__ void load_scales(const uint8_t *stage)
+    {
+        late = scale[MI - 1];
+        const float block = C::ROWS ? 1.f : *(const float *)(stage + at_sb);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            scale[i] = *(const float *)(stage + at_sa + i * 64) * block;
+    }
+    __device__ __forceinline__ void load_col(int j, const uint8_t *stage)
+    {
+        if constexpr (C::ROWS)
+            col[j] = *(const f32x4 *)(stage + at_sb + j * 16);
+    }
+    // Matrix instructions of step n of the k block.
+    template <int N> __device__ __forceinline__ void multiply()
+    {
+        constexpr int I = N * STEP / NI, J = N * STEP % NI;
+        if constexpr (C::EXACT) {
+            f32x4 c[STEP];
+#pragma unroll
+            for (int u = 0; u < STEP; ++u)
+                c[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int u = 0; u < STEP; ++u)
+                    c[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[J + u].v[q], a[I & 1].v[q], c[u], 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < STEP; ++u)
+                sums[N % RING][u] = c[u];
+        } else {
+            sums[N % RING][0] = block_sums(b[J], a[I & 1]);
+        }
+    }
+    // Add the scaled sums of step n; n < 0 counts from the end of the k block before.
+    template <int N> __device__ __forceinline__ void add()
+    {
+        constexpr int M = (N + STEPS) % STEPS, I = M * STEP / NI, J = M * STEP % NI;
+        const float s = N < 0 ? late : scale[I];
+#pragma unroll
+        for (int u = 0; u < STEP; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[I][J + u][r] = fmaf(sums[M % RING][u][r], C::ROWS ? s * col[J + u][r] : s, acc[I][J + u][r]);
+        // Used next a whole k block later, the sums would be moved down there, out from under the matrix instructions.
+#pragma unroll
+        for (int u = 0; u < STEP; ++u)
+            asm volatile("" : "+v"(acc[I][J + u]));
+    }
+};
+
 template <class C>
 __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8Args args)
 {
     using Loop = Fp8Loop<C>;
+    using Wave = Fp8Wave<C>;
     __shared__ __align__(1024) uint8_t smem[2 * C::STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const int l16 = lane & 15, g = lane >> 4;
-    const int a_at = (wm * C::WTM + l16) * 128 + ((g ^ Loop::swizzle_a(l16)) << 4);
-    const int b_row = wn * C::WTN + (l16 >> 2) * 16 + (l16 & 3);
-    const int b_at = C::A_BYTES + b_row * 128 + ((g ^ Loop::swizzle_b(b_row)) << 4);
+    Wave w;
+    w.init(wm, wn, lane);
     const int total = fp8_total_tiles(args, C::BM);
+    const uint32_t lds = lds_address(smem);
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         Fp8Tile tile;
         if (!fp8_find_tile(args, C::BM, C::BN, static_position(t, total, gridDim.x), tile))
             break;
         Loop loop;
         loop.setup(args, tile, tid);
-        f32x4 acc[C::MI][C::NI];
-#pragma unroll
-        for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-            for (int j = 0; j < C::NI; ++j)
-                acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        w.start_tile();
         barrier_lds(); // every wave has read the last tile's stages
-        const uint32_t lds = lds_address(smem);
-        if (args.nk > 0)
-            loop.issue(lds, 0, args.k);
-        for (int kb = 0; kb < args.nk; ++kb) {
-            uint8_t *stage = smem + (kb & 1) * C::STAGE;
-            wait_vmcnt<0>();
-            barrier_lds(); // this stage has landed for every wave, and every wave has read the other
-            if (args.k - kb * 128 < 128) {
-                Loop::clear_tail(stage, args.k - kb * 128, tid);
+        // A stage that has landed for every wave: its partial end is cleared.
+        auto enter = [&](uint8_t *stage, int kb) {
+            const int left = args.k - kb * 128;
+            if (left < 128) {
+                Loop::clear_tail(stage, left, tid);
                 barrier_lds();
             }
-            if (kb + 1 < args.nk)
-                loop.issue(lds + ((kb + 1) & 1) * C::STAGE, kb + 1, args.k);
-            const float *sa = (const float *)(stage + C::A_BYTES + C::B_BYTES) + wm * C::WTM + l16;
-            const float *sb = (const float *)(stage + C::A_BYTES + C::B_BYTES) + C::BM + wn * C::WTN;
-            Fragment<C::EXACT> b[C::NI];
-            f32x4 col[C::NI];
-#pragma unroll
-            for (int j = 0; j < C::NI; ++j) {
-                const i32x4 lo = *(const i32x4 *)(stage + b_at + j * 512);
-                const i32x4 hi = *(const i32x4 *)(stage + (b_at ^ 64) + j * 512);
-                b[j].set(lo, hi);
-                if constexpr (C::ROWS)
-                    col[j] = *(const f32x4 *)(sb + g * 16 + j * 4);
-            }
-            const float block = C::ROWS ? 1.0f : sb[0];
-#pragma unroll
-            for (int i = 0; i < C::MI; ++i) {
-                const i32x4 lo = *(const i32x4 *)(stage + a_at + i * 2048);
-                const i32x4 hi = *(const i32x4 *)(stage + (a_at ^ 64) + i * 2048);
-                Fragment<C::EXACT> a;
-                a.set(lo, hi);
-                const float s = sa[i * 16] * block;
-#pragma unroll
-                for (int j = 0; j < C::NI; ++j) {
-                    const f32x4 p = block_sums(b[j], a);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = fmaf(p[r], C::ROWS ? s * col[j][r] : s, acc[i][j][r]);
+        };
+        // One k block. LAST: none follows. Otherwise the next one's stage is
+        // taken over on the way, before the last row of blocks, and the loads of
+        // the block after that are started. STEADY: that one is whole, and its
+        // loads are started one by one between the matrix instructions from
+        // there into the next block (all at once they hold up every wave: 8192^3
+        // 520 us against 480); `pending` says that the block before did so.
+        bool pending = false;
+        auto k_block = [&](int kb, auto kind) {
+            constexpr bool MORE = kind.value != LAST, IN_STEPS = kind.value == STEADY;
+            constexpr int HANDOVER = Wave::STEPS - C::NI / Wave::STEP, PER_STEP = C::EXACT ? 2 : 1;
+            static_assert((Loop::PIECES + PER_STEP - 1) / PER_STEP <= Wave::STEPS, "started before the stage is waited for");
+            const uint32_t here = (kb & 1) * C::STAGE, there = C::STAGE - here;
+            const uint8_t *const stage = smem + here;
+            uint8_t *const next = smem + there;
+            static_for<Wave::STEPS>([&](auto n) {
+                constexpr int N = n.value, I = N * Wave::STEP / C::NI, J = N * Wave::STEP % C::NI;
+                if constexpr (J == 0 && I + 1 < C::MI)
+                    w.load_a((I + 1) & 1, I + 1, stage);
+                if constexpr (J == 0 && I + 1 == C::MI && MORE) {
+                    // Everything this wave needs of the stage is in registers: hand it back, take the next one.
+                    wait_vmcnt<0>();
+                    barrier_lds();
+                    if constexpr (!IN_STEPS) {
+                        if (kb + 2 < args.nk)
+                            loop.issue(lds + here, kb + 2, args.k);
+                        enter(next, kb + 1);
+                    }
+                    w.load_a((I + 1) & 1, 0, next);
+                }
+                w.template multiply<N>();
+                keep_order();
+                static_for<PER_STEP>([&](auto u) {
+                    if constexpr (N >= HANDOVER && IN_STEPS) {
+                        constexpr int I = (N - HANDOVER) * PER_STEP + u.value;
+                        if constexpr (I < Loop::PIECES)
+                            loop.template issue_piece<I>(lds + here, kb + 2);
+                    } else if constexpr (N < HANDOVER && MORE) {
+                        constexpr int I = (N + Wave::STEPS - HANDOVER) * PER_STEP + u.value;
+                        if constexpr (I < Loop::PIECES)
+                            if (pending)
+                                loop.template issue_piece<I>(lds + there, kb + 1);
+                    }
+                });
+                w.template add<N - Wave::LAG>();
+                if constexpr (I + 1 == C::MI && MORE)
+                    static_for<Wave::STEP>([&](auto u) { w.load_b(J + u.value, next); });
+                keep_order();
+            });
+            // ROWS: the sums in flight take the old column scales
+            if constexpr (C::ROWS || !MORE)
+                static_for<Wave::LAG>([&](auto n) { w.template add<Wave::STEPS + n.value - Wave::LAG>(); });
+            if constexpr (MORE) {
+                w.load_scales(next);
+                if constexpr (C::ROWS) {
+                    w.late = 0.f;
+                    static_for<C::NI>([&](auto j) { w.load_col(j.value, next); });
                 }
             }
+        };
+        if (args.nk > 0) {
+            loop.issue(lds, 0, args.k);
+            wait_vmcnt<0>();
+            barrier_lds();
+            if (args.nk > 1)
+                loop.issue(lds + C::STAGE, 1, args.k);
+            enter(smem, 0);
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j) {
+                w.load_b(j, smem);
+                w.load_col(j, smem);
+            }
+            w.load_a(0, 0, smem);
+            w.load_scales(smem);
+            const int whole = args.k / 128;
+            int kb = 0;
+            for (; kb + 2 < whole; ++kb) {
+                k_block(kb, IntC<STEADY>{});
+                pending = true;
+            }
+            for (; kb + 1 < args.nk; ++kb) {
+                k_block(kb, IntC<GENERAL>{});
+                pending = false;
+            }
+            k_block(kb, IntC<LAST>{});
         }
-        const int col0 = wn * C::WTN + g * 16;
+        const int col0 = wn * C::WTN + (lane >> 4) * 16;
 #pragma unroll
         for (int i = 0; i < C::MI; ++i) {
-            const int row = wm * C::WTM + i * 16 + l16;
+            const int row = wm * C::WTM + i * 16 + (lane & 15);
             if (row < tile.vm && col0 < tile.vn) {
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < C::NI; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        v[j * 4 + r] = acc[i][j][r];
+                        v[j * 4 + r] = w.acc[i][j][r];
                 fp8_store_row<C::BF16, 16>(args.d, (int64_t)(tile.row0 + row) * args.ldd + tile.col0 + col0, v,
                                            tile.vn - col0, args.d_vec);
             }
