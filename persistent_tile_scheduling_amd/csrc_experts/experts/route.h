@@ -22,7 +22,6 @@ constexpr int ROUTE_MAX_EXPERTS = 1024;
 constexpr int ROUTE_MAX_TOP = 32;
 constexpr int ROUTE_MAX_GROUPS = 64;
 constexpr float ROUTE_EPS = 1e-20f;
-constexpr int ORDER_LDS_WORDS = 6 * (ROUTE_MAX_EXPERTS + 1);
 
 struct RouteArgs {
     const void *logits;
@@ -63,95 +62,58 @@ __device__ __forceinline__ uint64_t sort_key(double x)
     return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-// The value of the lane D further on, for reductions over the lanes of a token:
-// within a row of 16 lanes by a DPP rotation, across rows by a shuffle.
-template <int D> __device__ __forceinline__ uint32_t partner(uint32_t v)
+// v combined with the value of another lane, so that after D = 8, 4, 2, 1 (and
+// 16, 32) every lane of a token has the combination of all: within a row of 16
+// lanes by a DPP rotation, across rows by the lane-swap instructions, which
+// leave both sides' values in two registers.
+template <int D, class F> __device__ __forceinline__ uint32_t reduce_step(uint32_t v, F f)
 {
-    if constexpr (D < 16)
-        return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + D, 0xF, 0xF, false);
-    else
-        return (uint32_t)__shfl_xor((int)v, D);
-}
-template <int D> __device__ __forceinline__ int partner(int v) { return (int)partner<D>((uint32_t)v); }
-template <int D> __device__ __forceinline__ float partner(float v)
-{
-    return __uint_as_float(partner<D>(__float_as_uint(v)));
-}
-template <int D> __device__ __forceinline__ uint64_t partner(uint64_t v)
-{
-    return (uint64_t)partner<D>((uint32_t)(v >> 32)) << 32 | partner<D>((uint32_t)v);
-}
-template <int D> __device__ __forceinline__ double partner(double v)
-{
-    return __longlong_as_double((long long)partner<D>((uint64_t)__double_as_longlong(v)));
-}
-
-// Candidates of the choice, larger first: by the logits, the 32-bit key above
-// the complement of the expert's index (a tie goes to the lowest index), or by
-// 64-bit scores with the index beside them. 0 in the key: none.
-template <bool WIDE> struct Candidate;
-template <> struct Candidate<false> {
-    uint64_t key;
-    __device__ __forceinline__ bool none() const { return key == 0; }
-    __device__ __forceinline__ int expert() const { return (int)~(uint32_t)key; }
-    __device__ __forceinline__ void take(const Candidate o) { key = o.key > key ? o.key : key; } // the better one
-    static __device__ __forceinline__ Candidate make(float x, double, int e)
-    {
-        return Candidate{(uint64_t)sort_key(x) << 32 | (uint32_t)~e};
+    if constexpr (D < 16) {
+        return f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + D, 0xF, 0xF, false));
+    } else {
+        const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                               : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return f(r[0], r[1]);
     }
-    static __device__ __forceinline__ Candidate nothing() { return Candidate{0}; }
-    template <int D> __device__ __forceinline__ Candidate from_partner() const { return Candidate{partner<D>(key)}; }
-};
-template <> struct Candidate<true> {
-    uint64_t key;
-    int index;
-    __device__ __forceinline__ bool none() const { return key == 0; }
-    __device__ __forceinline__ int expert() const { return index; }
-    __device__ __forceinline__ void take(const Candidate o)
-    {
-        const bool other = o.key > key || (o.key == key && o.index < index);
-        key = other ? o.key : key;
-        index = other ? o.index : index;
-    }
-    static __device__ __forceinline__ Candidate make(float, double c, int e) { return Candidate{sort_key(c), e}; }
-    static __device__ __forceinline__ Candidate nothing() { return Candidate{0, 0x7FFFFFFF}; }
-    template <int D> __device__ __forceinline__ Candidate from_partner() const
-    {
-        return Candidate{partner<D>(key), partner<D>(index)};
-    }
-};
-
-template <int LPT, class T, class F> __device__ __forceinline__ T reduce_lanes(T v, F f)
+}
+template <int LPT, class F> __device__ __forceinline__ uint32_t reduce_lanes(uint32_t v, F f)
 {
-    v = f(v, partner<8>(v));
-    v = f(v, partner<4>(v));
-    v = f(v, partner<2>(v));
-    v = f(v, partner<1>(v));
+    v = reduce_step<8>(v, f);
+    v = reduce_step<4>(v, f);
+    v = reduce_step<2>(v, f);
+    v = reduce_step<1>(v, f);
     if constexpr (LPT == 64) {
-        v = f(v, partner<16>(v));
-        v = f(v, partner<32>(v));
+        v = reduce_step<16>(v, f);
+        v = reduce_step<32>(v, f);
     }
     return v;
 }
+template <int LPT> __device__ __forceinline__ uint32_t max_lanes(uint32_t v)
+{
+    return reduce_lanes<LPT>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int LPT> __device__ __forceinline__ uint32_t min_lanes(uint32_t v)
+{
+    return reduce_lanes<LPT>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+template <int LPT> __device__ __forceinline__ float max_lanes(float v)
+{
+    return __uint_as_float(reduce_lanes<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
 template <int LPT> __device__ __forceinline__ float sum_lanes(float v)
 {
-    return reduce_lanes<LPT>(v, [](float a, float b) { return a + b; });
+    return __uint_as_float(reduce_lanes<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
-template <int LPT, int D, bool WIDE> __device__ __forceinline__ void take_better(Candidate<WIDE> &c)
+template <int LPT> __device__ __forceinline__ double sum_lanes(double v)
 {
-    c.take(c.template from_partner<D>());
-}
-template <int LPT, bool WIDE> __device__ __forceinline__ Candidate<WIDE> best_of_lanes(Candidate<WIDE> c)
-{
-    take_better<LPT, 8>(c);
-    take_better<LPT, 4>(c);
-    take_better<LPT, 2>(c);
-    take_better<LPT, 1>(c);
-    if constexpr (LPT == 64) {
-        take_better<LPT, 16>(c);
-        take_better<LPT, 32>(c);
-    }
-    return c;
+#pragma unroll
+    for (int d = 1; d < LPT; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
 }
 
 __device__ __forceinline__ float load_logit(const void *x, bool bf16, int64_t at)
@@ -163,65 +125,67 @@ __device__ __forceinline__ float load_logit(const void *x, bool bf16, int64_t at
 
 // Stable counting sort of the slots (token, j) by expert, in chunks of
 // consecutive slots; slots without an expert come last ("expert" E).
+constexpr int ORDER_WAVES = 8, ORDER_THREADS = 64 * ORDER_WAVES;
 
-// counts[e] = slots of expert e in [first, first + count), for the 256 threads.
-__device__ __forceinline__ void count_slots(const RouteArgs &args, int first, int count, int32_t *counts)
+__device__ __forceinline__ int slot_expert(const RouteArgs &args, int64_t slot)
 {
-    for (int e = threadIdx.x; e <= args.experts; e += 256)
-        counts[e] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < count; i += 256) {
-        const int e = args.ids[first + i];
-        atomicAdd(&counts[e < 0 ? args.experts : e], 1);
-    }
-    __syncthreads();
+    const int e = args.ids[slot];
+    return e < 0 ? args.experts : e;
 }
 
-// before[e] = total[0] + .. + total[e - 1] in LDS, by the first wave.
+__device__ __forceinline__ void place_slot(const RouteArgs &args, int slot, int expert, int p)
+{
+    args.rows[p] = slot / args.top;
+    args.positions[slot] = expert == args.experts ? -2 - p : p;
+}
+
+// before[e] = total[0] + .. + total[e - 1] in LDS, by the first wave: each lane
+// adds up a run of experts, and the runs are scanned across the lanes.
 __device__ __forceinline__ void scan_totals(const RouteArgs &args, const int32_t *total, int32_t *before)
 {
     if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        int base = 0;
-        for (int e0 = 0; e0 <= args.experts; e0 += 64) {
-            const int c = e0 + lane <= args.experts ? total[e0 + lane] : 0;
-            int sum = c;
+        const int lane = threadIdx.x, n = args.experts + 1, run = (n + 63) / 64;
+        const int lo = min(n, lane * run), hi = min(n, lo + run);
+        int sum = 0;
+        for (int e = lo; e < hi; ++e)
+            sum += total[e];
+        int at = sum;
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int v = __shfl_up(sum, d);
-                if (lane >= d)
-                    sum += v;
-            }
-            if (e0 + lane <= args.experts)
-                before[e0 + lane] = base + sum - c;
-            base += __shfl(sum, 63);
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(at, d);
+            if (lane >= d)
+                at += v;
+        }
+        at -= sum;
+        for (int e = lo; e < hi; ++e) {
+            before[e] = at;
+            at += total[e];
         }
     }
     __syncthreads();
 }
 
 // Place the slots [first, first + count): `at[e]` is the position of the first
-// of them with expert e. Wave w of the four takes the w-th quarter, 64 slots at
-// a time: a slot's rank among those is the number of lower lanes with the same
-// expert, found by one ballot per bit of the expert's index.
-__device__ __forceinline__ void place_slots(const RouteArgs &args, int first, int count, const int32_t *at,
+// of them with expert e. The waves take consecutive parts, 64 slots at a time:
+// a slot's rank among those is the number of lower lanes with the same expert,
+// found by one ballot per bit of the expert's index.
+__device__ __forceinline__ void place_slots(const RouteArgs &args, int64_t first, int count, const int32_t *at,
                                             int32_t *cursor)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = args.experts + 1;
-    for (int i = threadIdx.x; i < 4 * n; i += 256)
+    for (int i = threadIdx.x; i < ORDER_WAVES * n; i += ORDER_THREADS)
         cursor[i] = 0;
     __syncthreads();
-    const int quarter = (count + 255) / 256 * 64;
-    const int lo = min(count, wave * quarter), hi = min(count, lo + quarter);
+    const int part = (count + ORDER_THREADS - 1) / ORDER_THREADS * 64;
+    const int lo = min(count, wave * part), hi = min(count, lo + part);
     int32_t *const mine = cursor + wave * n;
-    for (int i = lo + lane; i < hi; i += 64) {
-        const int e = args.ids[first + i];
-        atomicAdd(&mine[e < 0 ? args.experts : e], 1);
-    }
+    for (int i = lo + lane; i < hi; i += 64)
+        atomicAdd(&mine[slot_expert(args, first + i)], 1);
     __syncthreads();
-    for (int e = threadIdx.x; e < n; e += 256) {
+    for (int e = threadIdx.x; e < n; e += ORDER_THREADS) {
         int p = at[e];
-        for (int w = 0; w < 4; ++w) {
+#pragma unroll
+        for (int w = 0; w < ORDER_WAVES; ++w) {
             const int c = cursor[w * n + e];
             cursor[w * n + e] = p;
             p += c;
@@ -231,9 +195,7 @@ __device__ __forceinline__ void place_slots(const RouteArgs &args, int first, in
     const int bits = 32 - __builtin_clz(args.experts);
     for (int i0 = lo; i0 < hi; i0 += 64) {
         const bool on = i0 + lane < hi;
-        const int slot = first + i0 + lane;
-        int e = on ? args.ids[slot] : 0;
-        e = e < 0 ? args.experts : e;
+        const int e = on ? slot_expert(args, first + i0 + lane) : 0;
         uint64_t same = __ballot(on);
         for (int b = 0; b < bits; ++b) {
             const bool bit = e >> b & 1;
@@ -246,8 +208,7 @@ __device__ __forceinline__ void place_slots(const RouteArgs &args, int first, in
             p = mine[e] + rank;
         wave_lds_exchange();
         if (on) {
-            args.rows[p] = slot / args.top;
-            args.positions[slot] = e == args.experts ? -2 - p : p;
+            place_slot(args, (int)(first + i0 + lane), e, p);
             if (rank == 0)
                 mine[e] = p + __builtin_popcountll(same);
         }
@@ -255,111 +216,139 @@ __device__ __forceinline__ void place_slots(const RouteArgs &args, int first, in
     }
 }
 
-__device__ __forceinline__ void store_offsets(const RouteArgs &args, const int32_t *before)
+__global__ __launch_bounds__(ORDER_THREADS) void order_count_kernel(const RouteArgs args)
 {
-    for (int e = threadIdx.x; e <= args.experts; e += 256)
-        args.offsets[e] = before[e];
-}
-
-// All slots in one workgroup.
-__device__ __forceinline__ void order_all(const RouteArgs &args, int32_t *lds)
-{
-    const int n = args.experts + 1, count = args.m * args.top;
-    count_slots(args, 0, count, lds);
-    scan_totals(args, lds, lds + n);
-    store_offsets(args, lds + n);
-    place_slots(args, 0, count, lds + n, lds + 2 * n);
-}
-
-__global__ __launch_bounds__(256) void order_all_kernel(const RouteArgs args)
-{
-    __shared__ int32_t lds[ORDER_LDS_WORDS];
-    order_all(args, lds);
-}
-
-__global__ __launch_bounds__(256) void order_count_kernel(const RouteArgs args)
-{
-    __shared__ int32_t lds[ROUTE_MAX_EXPERTS + 1];
+    __shared__ int32_t counts[ROUTE_MAX_EXPERTS + 1];
     const int64_t first = (int64_t)blockIdx.x * args.chunk, slots = (int64_t)args.m * args.top;
-    count_slots(args, (int)first, (int)min((int64_t)args.chunk, slots - first), lds);
-    for (int e = threadIdx.x; e <= args.experts; e += 256)
-        args.counts[(int64_t)blockIdx.x * (args.experts + 1) + e] = lds[e];
+    const int count = (int)min((int64_t)args.chunk, slots - first);
+    for (int e = threadIdx.x; e <= args.experts; e += ORDER_THREADS)
+        counts[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count; i += ORDER_THREADS)
+        atomicAdd(&counts[slot_expert(args, first + i)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= args.experts; e += ORDER_THREADS)
+        args.counts[(int64_t)blockIdx.x * (args.experts + 1) + e] = counts[e];
 }
 
-__global__ __launch_bounds__(256) void order_place_kernel(const RouteArgs args)
+// One chunk per workgroup. With several chunks each adds up all chunks' counts
+// itself (at most 256 x 1025 words, from L2), which saves a launch in between.
+__global__ __launch_bounds__(ORDER_THREADS) void order_place_kernel(const RouteArgs args)
 {
-    __shared__ int32_t lds[ORDER_LDS_WORDS];
-    const int n = args.experts + 1;
-    int32_t *const before = lds + n;
-    const int chunk = blockIdx.x;
-    int32_t mine[ROUTE_MAX_EXPERTS / 256 + 1]; // slots of this thread's experts in earlier chunks
+    __shared__ int32_t total[ROUTE_MAX_EXPERTS + 1], before[ROUTE_MAX_EXPERTS + 1];
+    __shared__ int32_t cursor[ORDER_WAVES * (ROUTE_MAX_EXPERTS + 1)];
+    constexpr int PER = ROUTE_MAX_EXPERTS / ORDER_THREADS + 1;
+    const int n = args.experts + 1, chunk = blockIdx.x;
+    const int64_t first = (int64_t)chunk * args.chunk, slots = (int64_t)args.m * args.top;
+    const int count = (int)min((int64_t)args.chunk, slots - first);
+    int32_t mine[PER]; // slots of this thread's experts in earlier chunks
+    if (args.chunks == 1) {
+        for (int e = threadIdx.x; e < n; e += ORDER_THREADS)
+            total[e] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < count; i += ORDER_THREADS)
+            atomicAdd(&total[slot_expert(args, i)], 1);
+    }
 #pragma unroll
-    for (int i = 0; i < ROUTE_MAX_EXPERTS / 256 + 1; ++i) {
-        const int e = i * 256 + threadIdx.x;
+    for (int i = 0; i < PER; ++i) {
+        const int e = i * ORDER_THREADS + threadIdx.x;
         mine[i] = 0;
-        if (e < n) {
-            int total = 0;
+        if (args.chunks > 1 && e < n) {
+            int sum = 0;
+#pragma unroll 16
             for (int c = 0; c < args.chunks; ++c) {
                 const int v = args.counts[(int64_t)c * n + e];
                 mine[i] += c < chunk ? v : 0;
-                total += v;
+                sum += v;
             }
-            lds[e] = total;
+            total[e] = sum;
         }
     }
     __syncthreads();
-    scan_totals(args, lds, before);
+    scan_totals(args, total, before);
     if (chunk == 0)
-        store_offsets(args, before);
+        for (int e = threadIdx.x; e < n; e += ORDER_THREADS)
+            args.offsets[e] = before[e];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ROUTE_MAX_EXPERTS / 256 + 1; ++i)
-        if (i * 256 + threadIdx.x < n)
-            before[i * 256 + threadIdx.x] += mine[i];
+    for (int i = 0; i < PER; ++i)
+        if (i * ORDER_THREADS + threadIdx.x < n)
+            before[i * ORDER_THREADS + threadIdx.x] += mine[i];
     __syncthreads();
-    const int64_t first = (int64_t)chunk * args.chunk, slots = (int64_t)args.m * args.top;
-    place_slots(args, (int)first, (int)min((int64_t)args.chunk, slots - first), before, lds + 2 * n);
+    place_slots(args, first, count, before, cursor);
+}
+
+// Few slots, their experts in LDS (E for none), by the 256 threads of the one
+// workgroup that has routed them: each slot's position and each offset is a
+// count over all slots, with no atomics and nothing to wait for in between.
+constexpr int ROUTE_FUSED_SLOTS = 128;
+__device__ __forceinline__ void order_few(const RouteArgs &args, const int32_t *experts, int count)
+{
+    for (int i = threadIdx.x; i < max(count, args.experts + 1); i += 256) {
+        const int mine = i < count ? experts[i] : 0;
+        int position = 0, offset = 0;
+#pragma unroll 8
+        for (int j = 0; j < count; ++j) {
+            const int e = experts[j];
+            position += e < mine || (e == mine && j < i);
+            offset += e < i;
+        }
+        if (i < count)
+            place_slot(args, i, mine, position);
+        if (i <= args.experts)
+            args.offsets[i] = offset;
+    }
 }
 
 // ---- choice -------------------------------------------------------------------
 
 // The groups that stay, bit g for group g. `c` holds the token's scores in LDS
-// (-inf where closed); a lane scores the groups lane, lane + LPT, ...
+// (-inf where closed). Each group is scored by as many lanes as there are to
+// spare (a power of two), or each lane scores several groups.
 template <int LPT>
 __device__ __forceinline__ uint64_t keep_groups(const RouteArgs &args, double *c, int lane)
 {
     constexpr int GPL = ROUTE_MAX_GROUPS / LPT;
     const int size = args.experts / args.groups;
+    int spare = 1;
+    while (2 * spare * args.groups <= LPT)
+        spare *= 2;
     double mine[GPL];
 #pragma unroll
     for (int q = 0; q < GPL; ++q) {
-        const int g = q * LPT + lane;
+        const int g = q * LPT + lane / spare;
         double first = -INFINITY, second = -INFINITY;
         if (g < args.groups)
-            for (int i = 0; i < size; ++i) {
+            for (int i = lane % spare; i < size; i += spare) {
                 const double s = c[g * size + i];
                 second = fmax(second, fmin(first, s));
                 first = fmax(first, s);
             }
+        for (int d = 1; d < spare; d *= 2) {
+            const double f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+            second = fmax(fmin(first, f), fmax(second, s));
+            first = fmax(first, f);
+        }
         mine[q] = args.pair && second > -INFINITY ? first + second : first;
     }
     wave_lds_exchange();
 #pragma unroll
     for (int q = 0; q < GPL; ++q)
-        if (q * LPT + lane < args.groups)
-            c[q * LPT + lane] = mine[q];
+        if (lane % spare == 0 && q * LPT + lane / spare < args.groups)
+            c[q * LPT + lane / spare] = mine[q];
     wave_lds_exchange();
     uint64_t kept = 0;
-    for (int g = 0; g < args.groups; ++g) {
-        const double s = c[g];
-        int ahead = 0; // groups that come before g
+    const int shift = (threadIdx.x & 63) & ~(LPT - 1); // this token's lanes in a ballot
 #pragma unroll
-        for (int q = 0; q < GPL; ++q) {
-            const int h = q * LPT + lane;
-            ahead += h < args.groups && (mine[q] > s || (mine[q] == s && h < g));
-        }
-        ahead = reduce_lanes<LPT>(ahead, [](int a, int b) { return a + b; });
-        kept |= (uint64_t)(ahead < args.keep) << g;
+    for (int q = 0; q < GPL; ++q) { // lane g for group g
+        const int g = q * LPT + lane;
+        const double s = g < args.groups ? c[g] : 0.;
+        int ahead = 0; // groups that come before g
+#pragma unroll 8
+        for (int h = 0; h < args.groups; ++h)
+            ahead += c[h] > s || (c[h] == s && h < g);
+        const uint64_t stays = __ballot(g < args.groups && ahead < args.keep) >> shift;
+        kept |= (LPT == 64 ? stays : stays & ((1ull << (LPT & 63)) - 1)) << (q * LPT & 63);
     }
     wave_lds_exchange();
     return kept;
@@ -372,7 +361,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
 {
     constexpr int TOKENS = 256 / LPT; // per workgroup and pass
     constexpr int CHOICE_BYTES = TOKENS * LPT * VPL * 8;
-    __shared__ __align__(8) uint8_t lds[CHOICE_BYTES > ORDER_LDS_WORDS * 4 ? CHOICE_BYTES : ORDER_LDS_WORDS * 4];
+    __shared__ __align__(8) uint8_t lds[CHOICE_BYTES];
+    __shared__ int32_t fused_experts[ROUTE_FUSED_SLOTS];
     const int lane = threadIdx.x & (LPT - 1), slot = threadIdx.x / LPT;
     double *const scores = (double *)lds + slot * LPT * VPL;
     const int experts = args.experts;
@@ -386,7 +376,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
             x[v] = live && e < experts ? load_logit(args.logits, args.bf16, token * args.ld + e) : -INFINITY;
             top = fmaxf(top, x[v]);
         }
-        top = reduce_lanes<LPT>(top, [](float a, float b) { return fmaxf(a, b); });
+        top = max_lanes<LPT>(top);
         top = top == -INFINITY ? 0.f : top;
         float total = 1.f; // the softmax's denominator
         if (!args.sigmoid) {
@@ -408,7 +398,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
                     c[v] = exp((double)x[v] - (double)top);
                     all += c[v];
                 }
-                all = reduce_lanes<LPT>(all, [](double a, double b) { return a + b; });
+                all = sum_lanes<LPT>(all);
                 all = all == 0. ? 1. : all;
             }
 #pragma unroll
@@ -425,42 +415,57 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
             for (int v = 0; v < VPL; ++v)
                 c[v] = (double)x[v];
         }
-        Candidate<WIDE> cand[VPL];
+        uint32_t key[VPL], low[VPL]; // of c, or of the logits alone; key 0: closed
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            cand[v] = x[v] > -INFINITY && c[v] > -INFINITY ? Candidate<WIDE>::make(x[v], c[v], v * LPT + lane)
-                                                           : Candidate<WIDE>::nothing();
+        for (int v = 0; v < VPL; ++v) {
+            const bool open = x[v] > -INFINITY && c[v] > -INFINITY;
+            const uint64_t k = WIDE ? sort_key(c[v]) : (uint64_t)sort_key(x[v]) << 32;
+            key[v] = open ? (uint32_t)(k >> 32) : 0u;
+            low[v] = (uint32_t)k;
+        }
         if (args.groups > 1) {
             const int size = experts / args.groups;
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
-                scores[v * LPT + lane] = cand[v].none() ? -INFINITY : c[v];
+                scores[v * LPT + lane] = key[v] == 0 ? -INFINITY : c[v];
             wave_lds_exchange();
             const uint64_t kept = keep_groups<LPT>(args, scores, lane);
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
                 if (!(kept >> (min(v * LPT + lane, experts - 1) / size) & 1))
-                    cand[v].key = 0;
+                    key[v] = 0;
         }
-        // the best ones in turn; slot j belongs to lane j % 16 (of every row of lanes)
+        // The best ones in turn: the largest key, of those the largest low half, of those the lowest index. Slot j
+        // belongs to lane j % 16 (of every row of lanes).
         int id[ROUTE_MAX_TOP / 16];
 #pragma unroll
         for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
             id[q] = -1;
         for (int j = 0; j < args.top; ++j) {
-            Candidate<WIDE> best = cand[0];
+            uint32_t best = key[0];
 #pragma unroll
             for (int v = 1; v < VPL; ++v)
-                best.take(cand[v]);
-            best = best_of_lanes<LPT>(best);
-            const int e = best.none() ? -1 : best.expert();
+                best = max(best, key[v]);
+            best = max_lanes<LPT>(best);
+            uint32_t best_low = 0;
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    best_low = max(best_low, key[v] == best ? low[v] : 0u);
+                best_low = max_lanes<LPT>(best_low);
+            }
+            uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+            for (int v = VPL - 1; v >= 0; --v)
+                at = key[v] == best && (!WIDE || low[v] == best_low) ? (uint32_t)(v * LPT + lane) : at;
+            at = min_lanes<LPT>(at);
+            const int e = best == 0 ? -1 : (int)at;
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
-                cand[v].key = v * LPT + lane == e ? 0 : cand[v].key;
+                key[v] = v * LPT + lane == e ? 0u : key[v];
 #pragma unroll
             for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
-                if (j == q * 16 + (lane & 15))
-                    id[q] = e;
+                id[q] = j == q * 16 + (lane & 15) ? e : id[q];
         }
         float p[ROUTE_MAX_TOP / 16], sum = 0.f;
 #pragma unroll
@@ -478,15 +483,17 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
 #pragma unroll
             for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
                 if (q * 16 + lane < args.top) {
-                    args.ids[token * args.top + q * 16 + lane] = id[q];
-                    args.weights[token * args.top + q * 16 + lane] = id[q] < 0 ? 0.f : p[q] * factor;
+                    const int64_t at = token * args.top + q * 16 + lane;
+                    args.ids[at] = id[q];
+                    args.weights[at] = id[q] < 0 ? 0.f : p[q] * factor;
+                    if (args.fused)
+                        fused_experts[at] = id[q] < 0 ? experts : id[q];
                 }
         }
     }
     if (args.fused) { // this workgroup has had every token
-        __threadfence_block();
         __syncthreads();
-        order_all(args, (int32_t *)lds);
+        order_few(args, fused_experts, args.m * args.top);
     }
 }
 

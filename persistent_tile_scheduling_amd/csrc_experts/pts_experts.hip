@@ -173,7 +173,7 @@ int32_t vector_rows(const void *d, int64_t ldd, int32_t dtype)
 // slots each, at most 256 workgroups (each adds up every chunk's counts).
 void order_chunks(int64_t slots, int64_t *chunk, int64_t *chunks)
 {
-    *chunk = std::max<int64_t>(2048, ceil_div(ceil_div(slots, 256), 256) * 256);
+    *chunk = std::max<int64_t>(2048, ceil_div(ceil_div(slots, 256), 512) * 512);
     *chunks = ceil_div(slots, *chunk);
 }
 
@@ -364,16 +364,16 @@ gemm_status pts_moe_route(const void *logits, int32_t dtype, int64_t ld, const f
                         experts, top, groups, topk_groups, dtype == GEMM_DTYPE_BF16, score == PTS_SCORE_SIGMOID,
                         group_top2 != 0, renormalize != 0, 0, (int32_t)chunk, (int32_t)chunks, scale};
     // few tokens: one workgroup routes them all and orders their slots, one launch for both
-    args.fused = offsets != nullptr && m <= 16;
+    args.fused = offsets != nullptr && m <= 16 && m * top <= pts::ROUTE_FUSED_SLOTS;
     if (m > 0 || args.fused) {
         st = bias != nullptr ? launch_route<true>(args, cus, stream) : launch_route<false>(args, cus, stream);
         if (st != GEMM_OK || offsets == nullptr || args.fused)
             return st;
     }
-    if (chunks == 1)
-        return launch(&pts::order_all_kernel, dim3(1), 256, args, stream);
-    st = launch(&pts::order_count_kernel, dim3((uint32_t)chunks), 256, args, stream);
-    return st != GEMM_OK ? st : launch(&pts::order_place_kernel, dim3((uint32_t)chunks), 256, args, stream);
+    if (chunks > 1)
+        st = launch(&pts::order_count_kernel, dim3((uint32_t)chunks), pts::ORDER_THREADS, args, stream);
+    return st != GEMM_OK ? st
+                         : launch(&pts::order_place_kernel, dim3((uint32_t)chunks), pts::ORDER_THREADS, args, stream);
 }
 
 gemm_status pts_moe_route_backward(const float *dweights, const void *logits, int32_t dtype, int64_t ld,

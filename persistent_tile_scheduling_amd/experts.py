@@ -88,23 +88,20 @@ def pts_moe_combine_backward(*args, stream=None) -> None:
 # Tensors
 # ---------------------------------------------------------------------------
 
+# The checks below stand in the way of kernels of a few microseconds: each call
+# tests its arguments inline and only then asks the functions here to say what is
+# wrong.
+
 _DTYPES = {torch.bfloat16: GEMM_DTYPE_BF16, torch.float32: GEMM_DTYPE_F32}
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+_VALUES = tuple(_DTYPES)
 _raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _device(**tensors) -> int:
-    """The current device's index; every tensor must be on it."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, t in tensors.items():
-        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0):
-            where = t.device if isinstance(t, torch.Tensor) else type(t).__name__
-            raise ValueError(f"{name} is on {where}, not on the current GPU")
-    return dev
+_current = torch._C._cuda_getDevice
+_empty = torch.empty_strided
 
 
 def _expect(name, t, dtypes, shape) -> None:
-    """dtype and shape (None: any extent) of a tensor."""
+    """Refuse a tensor that has not one of the dtypes and the shape (None: any extent)."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != len(shape) or any(
             want is not None and have != want for have, want in zip(t.shape, shape)):
         have = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
@@ -113,21 +110,64 @@ def _expect(name, t, dtypes, shape) -> None:
                          f"not {have}")
 
 
+def _matrix(name, t, dtypes) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2:
+        _expect(name, t, dtypes, (None, None))
+
+
+def _exactly(name, t, dtype, shape) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        _expect(name, t, (dtype,), shape)
+
+
+def _index(name, t, shape) -> None:
+    """A contiguous int32 tensor."""
+    _exactly(name, t, _I32, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _weights(name, t, shape) -> None:
+    """A contiguous fp32 tensor."""
+    _exactly(name, t, _F32, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _device(first, *others) -> int:
+    """The current device's index; every tensor must be on it."""
+    dev = first.get_device()
+    if dev < 0 or dev != _current():
+        raise ValueError(f"tensors are on {first.device}, not on the current GPU")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, not on the current GPU ({first.device})")
+    return dev
+
+
 def _leading(name, t, of: int = 1) -> int:
     """Row stride of a row-major matrix (the last two dimensions); for a single row its width, rounded up to `of`."""
     rows, width = t.shape[-2], t.shape[-1]
-    if t.numel() and width > 1 and t.stride(-1) != 1:
+    if rows > 1 and width > 1:
+        row, col = t.stride(-2), t.stride(-1)
+        if col != 1 or row < width:
+            raise ValueError(f"{name} must have unit stride along its rows and rows that do not overlap, "
+                             f"not strides {t.stride()}")
+        return row
+    if width > 1 and rows and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit stride along its rows")
-    if rows <= 1 or not t.numel():
-        return (width + of - 1) // of * of
-    if t.stride(-2) < width:
-        raise ValueError(f"{name}'s row stride {t.stride(-2)} is below its width {width}")
-    return t.stride(-2)
+    if rows > 1 and width:
+        if t.stride(-2) < 1:
+            raise ValueError(f"{name}'s rows overlap")
+        return t.stride(-2)
+    return (width + of - 1) // of * of
 
 
-def _contiguous(name, t) -> None:
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+_BLOCKS = {(1, 128): 1, (128, 128): 128}
+_quantize, _gemm, _gemm_experts = _lib.pts_quantize_fp8, _lib.pts_gemm_fp8, _lib.pts_gemm_fp8_experts
+_route_workspace, _route, _route_backward = (_lib.pts_moe_route_workspace, _lib.pts_moe_route,
+                                             _lib.pts_moe_route_backward)
+_combine, _combine_backward = _lib.pts_moe_combine, _lib.pts_moe_combine_backward
 
 
 def quantize_fp8(x: torch.Tensor, block=(1, 128), swiglu: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
@@ -142,51 +182,47 @@ def quantize_fp8(x: torch.Tensor, block=(1, 128), swiglu: bool = False) -> tuple
     (ceil(m / 128), ceil(k / 128)). scale = max(max |x| / 448, 2^-126); a block
     with an infinity or a NaN comes out NaN.
     """
-    _expect("x", x, (torch.bfloat16, torch.float32), (None, None))
-    block = tuple(block)
-    if block not in ((1, 128), (128, 128)):
+    _matrix("x", x, _VALUES)
+    tall = _BLOCKS.get(block if type(block) is tuple else tuple(block))
+    if tall is None:
         raise ValueError(f"block must be (1, 128) or (128, 128), not {block}")
-    dev = _device(x=x)
+    dev, device = _device(x), x.device
     m, k = x.shape
     row, col = x.stride()
-    layout = GEMM_ROW_MAJOR
-    if k > 1 and col != 1 and x.numel():
-        if m > 1 and row != 1:
-            raise ValueError("x must be contiguous along one of its dimensions")
-        layout = GEMM_COL_MAJOR
-    ld = (col if layout == GEMM_COL_MAJOR else row) if m > 1 and x.numel() else max(k, 1)
-    if layout == GEMM_COL_MAJOR:
-        ld = col
-    if x.numel() and ld < (m if layout == GEMM_COL_MAJOR else k):
-        raise ValueError("x's rows overlap")
+    if col == 1 or k <= 1 or m == 0:
+        layout, ld = GEMM_ROW_MAJOR, row if m > 1 and k else k
+    elif row == 1 or m == 1:
+        layout, ld = GEMM_COL_MAJOR, col
+    else:
+        raise ValueError(f"x must be contiguous along one of its dimensions, not strides {x.stride()}")
+    if ld < (k if layout == GEMM_ROW_MAJOR else m):
+        raise ValueError(f"x's rows overlap (strides {x.stride()})")
     if swiglu:
         if k % 2:
             raise ValueError(f"the gated form takes an even width, not {k}")
         k //= 2
-    kb = (k + 127) // 128
-    wide = (k + 15) // 16 * 16
-    q = torch.empty((m, wide), dtype=_E4M3, device=x.device)
-    if block[0] == 1:
-        scale = torch.empty((kb, m), dtype=torch.float32, device=x.device).t()
+    kb, wide = (k + 127) // 128, (k + 15) // 16 * 16
+    q = _empty((m, k), (wide, 1), dtype=_E4M3, device=device) if wide == k else \
+        torch.empty((m, wide), dtype=_E4M3, device=device)[:, :k]
+    if tall == 1:
+        scale, sm, sk = _empty((m, kb), (1, m), dtype=_F32, device=device), 1, m or 1
     else:
-        scale = torch.empty(((m + 127) // 128, kb), dtype=torch.float32, device=x.device)
-    _check(_lib.pts_quantize_fp8(x.data_ptr(), _DTYPES[x.dtype], layout, m, k, ld, block[0], 1 if swiglu else 0,
-                                 q.data_ptr(), wide, scale.data_ptr(), max(scale.stride(0), 1), max(scale.stride(1), 1),
-                                 _raw_stream(dev)))
-    return (q if wide == k else q[:, :k]), scale
-
-
-def _scale_strides(t) -> tuple[int, int]:
-    return t.stride(-2) if t.shape[-2] > 1 else 0, t.stride(-1) if t.shape[-1] > 1 else 0
+        mb = (m + 127) // 128
+        scale, sm, sk = _empty((mb, kb), (kb, 1), dtype=_F32, device=device), kb or 1, 1
+    status = _quantize(x.data_ptr(), _DTYPES[x.dtype], layout, m, k, ld, tall, 1 if swiglu else 0, q.data_ptr(), wide,
+                       scale.data_ptr(), sm, sk, _raw_stream(dev))
+    if status:
+        _check(status)
+    return q, scale
 
 
 def _output(out, m, n, out_dtype, device):
+    """The result's tensor and row stride."""
     if out is None:
         if out_dtype not in _DTYPES:
             raise ValueError(f"out_dtype must be float32 or bfloat16, not {out_dtype}")
-        out = torch.empty((m, n), dtype=out_dtype, device=device)
-    else:
-        _expect("out", out, tuple(_DTYPES), (m, n))
+        return _empty((m, n), (n, 1), dtype=out_dtype, device=device), n
+    _expect("out", out, _VALUES, (m, n))
     return out, _leading("out", out)
 
 
@@ -206,19 +242,26 @@ def gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     ``gemm_fp8(*quantize_fp8(dd), *quantize_fp8(b_t, (128, 128)))`` and
     dB^T = dD^T . A is ``gemm_fp8(*quantize_fp8(dd.t()), *quantize_fp8(a.t()))``.
     """
-    _expect("a", a, (_E4M3,), (None, None))
+    _matrix("a", a, (_E4M3,))
+    _matrix("b", b, (_E4M3,))
     m, k = a.shape
-    _expect("b", b, (_E4M3,), (None, k))
     n, kb = b.shape[0], (k + 127) // 128
-    _expect("a_scale", a_scale, (torch.float32,), (m, kb))
-    blocks = b_scale.dim() == 2 and b_scale.shape[0] == (n + 127) // 128
-    _expect("b_scale", b_scale, (torch.float32,), ((n + 127) // 128 if blocks else n, kb))
-    dev = _device(a=a, a_scale=a_scale, b=b, b_scale=b_scale, out=out)
-    out, ldd = _output(out, m, n, out_dtype, a.device)
-    _check(_lib.pts_gemm_fp8(a.data_ptr(), _leading("a", a, 16), a_scale.data_ptr(), *_scale_strides(a_scale),
-                             b.data_ptr(), _leading("b", b, 16), b_scale.data_ptr(), *_scale_strides(b_scale),
-                             128 if blocks else 1, out.data_ptr(), ldd, _DTYPES[out.dtype], m, n, k, _raw_stream(dev)))
-    return out
+    if b.shape[1] != k:
+        raise ValueError(f"a and b have {k} and {b.shape[1]} columns")
+    _exactly("a_scale", a_scale, _F32, (m, kb))
+    blocks = isinstance(b_scale, torch.Tensor) and b_scale.shape == ((n + 127) // 128, kb)
+    _exactly("b_scale", b_scale, _F32, b_scale.shape if blocks else (n, kb))
+    dev = _device(a, a_scale, b, b_scale, out)
+    d, ldd = _output(out, m, n, out_dtype, a.device)
+    sam, sak = a_scale.stride()
+    sbn, sbk = b_scale.stride()
+    status = _gemm(a.data_ptr(), _leading("a", a, 16), a_scale.data_ptr(), sam if m > 1 else 0, sak if kb > 1 else 0,
+                   b.data_ptr(), _leading("b", b, 16), b_scale.data_ptr(), sbn if b_scale.shape[0] > 1 else 0,
+                   sbk if kb > 1 else 0, 128 if blocks else 1, d.data_ptr(), ldd, _DTYPES[d.dtype], m, n, k,
+                   _raw_stream(dev))
+    if status:
+        _check(status)
+    return d
 
 
 def gemm_fp8_experts(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
@@ -233,29 +276,31 @@ def gemm_fp8_experts(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
     :func:`moe_route` returns both), or None: row i reads row i. Rows in no
     expert's range are left as they were (in a new result: not set).
     """
-    _expect("a", a, (_E4M3,), (None, None))
+    _matrix("a", a, (_E4M3,))
     have, k = a.shape
-    _expect("b", b, (_E4M3,), (None, None, k))
-    experts, n = b.shape[:2]
-    kb = (k + 127) // 128
-    _expect("a_scale", a_scale, (torch.float32,), (have, kb))
-    _expect("b_scale", b_scale, (torch.float32,), (experts, (n + 127) // 128, kb))
-    _expect("offsets", offsets, (torch.int32,), (experts + 1,))
-    _contiguous("offsets", offsets)
+    if not isinstance(b, torch.Tensor) or b.dtype is not _E4M3 or b.dim() != 3 or b.shape[2] != k:
+        _expect("b", b, (_E4M3,), (None, None, k))
+    experts, n, kb = b.shape[0], b.shape[1], (k + 127) // 128
+    _exactly("a_scale", a_scale, _F32, (have, kb))
+    _exactly("b_scale", b_scale, _F32, (experts, (n + 127) // 128, kb))
+    _index("offsets", offsets, (experts + 1,))
     m, index = have, None
     if rows is not None:
-        _expect("rows", rows, (torch.int32,), (None,))
-        _contiguous("rows", rows)
+        _expect("rows", rows, (_I32,), (None,))
+        _index("rows", rows, rows.shape)
         m, index = rows.shape[0], rows.data_ptr()
-    dev = _device(a=a, a_scale=a_scale, b=b, b_scale=b_scale, offsets=offsets, rows=rows, out=out)
-    out, ldd = _output(out, m, n, out_dtype, a.device)
-    _check(_lib.pts_gemm_fp8_experts(a.data_ptr(), have, _leading("a", a, 16), a_scale.data_ptr(),
-                                     *_scale_strides(a_scale), b.data_ptr(), _leading("b", b, 16),
-                                     b.stride(0) if experts > 1 else 0, b_scale.data_ptr(),
-                                     b_scale.stride(0) if experts > 1 else 0, *_scale_strides(b_scale), experts,
-                                     offsets.data_ptr(), index, out.data_ptr(), ldd, _DTYPES[out.dtype], m, n, k,
-                                     _raw_stream(dev)))
-    return out
+    dev = _device(a, a_scale, b, b_scale, offsets, rows, out)
+    d, ldd = _output(out, m, n, out_dtype, a.device)
+    sam, sak = a_scale.stride()
+    sbe, sbn, sbk = b_scale.stride()
+    status = _gemm_experts(a.data_ptr(), have, _leading("a", a, 16), a_scale.data_ptr(), sam if have > 1 else 0,
+                           sak if kb > 1 else 0, b.data_ptr(), _leading("b", b, 16), b.stride(0) if experts > 1 else 0,
+                           b_scale.data_ptr(), sbe if experts > 1 else 0, sbn if n > 128 else 0, sbk if kb > 1 else 0,
+                           experts, offsets.data_ptr(), index, d.data_ptr(), ldd, _DTYPES[d.dtype], m, n, k,
+                           _raw_stream(dev))
+    if status:
+        _check(status)
+    return d
 
 
 class MoeRouting(NamedTuple):
@@ -287,30 +332,30 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: tor
     expert to a token; a row of them (a padded token) gets ids -1, weights 0 and
     rows behind ``offsets[-1]``.
     """
-    _expect("logits", logits, (torch.bfloat16, torch.float32), (None, None))
+    _matrix("logits", logits, _VALUES)
     m, experts = logits.shape
     if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, group_score one of {sorted(_GROUP_SCORES)}")
     if bias is not None:
-        _expect("bias", bias, (torch.float32,), (experts,))
-        _contiguous("bias", bias)
-    dev = _device(logits=logits, bias=bias)
-    ld = _leading("logits", logits)
-    device, top = logits.device, int(k)
+        _weights("bias", bias, (experts,))
+    top = int(k)
     if not 1 <= top <= experts:
         raise ValueError(f"k must be in [1, {experts}], not {k}")
-    ids = torch.empty((m, top), dtype=torch.int32, device=device)
-    weights = torch.empty((m, top), dtype=torch.float32, device=device)
-    offsets = torch.empty((experts + 1,), dtype=torch.int32, device=device)
-    rows = torch.empty((m * top,), dtype=torch.int32, device=device)
-    positions = torch.empty((m, top), dtype=torch.int32, device=device)
-    need = _lib.pts_moe_route_workspace(m, experts, top)
-    work = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
-    _check(_lib.pts_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], ld, None if bias is None else bias.data_ptr(), m,
-                              experts, top, _SCORES[score], groups, topk_groups, _GROUP_SCORES[group_score],
-                              1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-                              rows.data_ptr(), positions.data_ptr(), None if work is None else work.data_ptr(), need,
-                              _raw_stream(dev)))
+    dev, device, ld = _device(logits, bias), logits.device, _leading("logits", logits)
+    ids = _empty((m, top), (top, 1), dtype=_I32, device=device)
+    weights = _empty((m, top), (top, 1), dtype=_F32, device=device)
+    offsets = _empty((experts + 1,), (1,), dtype=_I32, device=device)
+    rows = _empty((m * top,), (1,), dtype=_I32, device=device)
+    positions = _empty((m, top), (top, 1), dtype=_I32, device=device)
+    need, work = _route_workspace(m, experts, top), None
+    if need:
+        work = _empty((need,), (1,), dtype=torch.uint8, device=device)
+    status = _route(logits.data_ptr(), _DTYPES[logits.dtype], ld, None if bias is None else bias.data_ptr(), m, experts, top,
+                    _SCORES[score], groups, topk_groups, _GROUP_SCORES[group_score], 1 if renormalize else 0, scale,
+                    ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), positions.data_ptr(),
+                    None if work is None else work.data_ptr(), need, _raw_stream(dev))
+    if status:
+        _check(status)
     return MoeRouting(ids, weights, offsets, rows, positions)
 
 
@@ -319,37 +364,38 @@ def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.
     """The gradient of the logits (their dtype and shape) from that of
     :func:`moe_route`'s weights; ``ids``, ``score``, ``renormalize`` and ``scale``
     as in the forward call. The choice, and with it the bias, has no gradient."""
-    _expect("logits", logits, (torch.bfloat16, torch.float32), (None, None))
+    _matrix("logits", logits, _VALUES)
     m, experts = logits.shape
-    _expect("ids", ids, (torch.int32,), (m, None))
+    _matrix("ids", ids, (_I32,))
     top = ids.shape[1]
-    _expect("dweights", dweights, (torch.float32,), (m, top))
+    _index("ids", ids, (m, top))
+    _weights("dweights", dweights, (m, top))
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    _contiguous("ids", ids)
-    _contiguous("dweights", dweights)
-    dev = _device(dweights=dweights, logits=logits, ids=ids)
-    out = torch.empty((m, experts), dtype=logits.dtype, device=logits.device)
-    _check(_lib.pts_moe_route_backward(dweights.data_ptr(), logits.data_ptr(), _DTYPES[logits.dtype],
-                                       _leading("logits", logits), ids.data_ptr(), m, experts, top, _SCORES[score],
-                                       1 if renormalize else 0, scale, out.data_ptr(), experts, _raw_stream(dev)))
+    dev, ld = _device(logits, dweights, ids), _leading("logits", logits)
+    out = _empty((m, experts), (experts, 1), dtype=logits.dtype, device=logits.device)
+    status = _route_backward(dweights.data_ptr(), logits.data_ptr(), _DTYPES[logits.dtype], ld, ids.data_ptr(), m, experts,
+                             top, _SCORES[score], 1 if renormalize else 0, scale, out.data_ptr(), experts, _raw_stream(dev))
+    if status:
+        _check(status)
     return out
 
 
 def moe_combine(y: torch.Tensor, weights: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
     """out[t] = sum over j of ``weights[t, j] * y[positions[t, j]]``, in fp32, in
     ``y``'s dtype (bf16 or fp32). A position outside ``y`` adds nothing."""
-    _expect("y", y, (torch.bfloat16, torch.float32), (None, None))
-    _expect("positions", positions, (torch.int32,), (None, None))
+    _matrix("y", y, _VALUES)
+    _matrix("positions", positions, (_I32,))
     m, top = positions.shape
-    _expect("weights", weights, (torch.float32,), (m, top))
-    _contiguous("positions", positions)
-    _contiguous("weights", weights)
-    dev = _device(y=y, weights=weights, positions=positions)
+    _index("positions", positions, (m, top))
+    _weights("weights", weights, (m, top))
     rows, n = y.shape
-    out = torch.empty((m, n), dtype=y.dtype, device=y.device)
-    _check(_lib.pts_moe_combine(y.data_ptr(), _DTYPES[y.dtype], _leading("y", y), rows, weights.data_ptr(),
-                                positions.data_ptr(), m, n, top, out.data_ptr(), n, _raw_stream(dev)))
+    dev, ld = _device(y, weights, positions), _leading("y", y)
+    out = _empty((m, n), (n, 1), dtype=y.dtype, device=y.device)
+    status = _combine(y.data_ptr(), _DTYPES[y.dtype], ld, rows, weights.data_ptr(), positions.data_ptr(), m, n, top,
+                      out.data_ptr(), n, _raw_stream(dev))
+    if status:
+        _check(status)
     return out
 
 
@@ -359,20 +405,20 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Ten
     slot's (as :func:`moe_route` numbers them: the rows of slots without an
     expert get a gradient of 0); a row that no position names is not set. No two
     slots may name the same row."""
-    _expect("y", y, (torch.bfloat16, torch.float32), (None, None))
-    _expect("positions", positions, (torch.int32,), (None, None))
+    _matrix("y", y, _VALUES)
+    _matrix("positions", positions, (_I32,))
     m, top = positions.shape
     rows, n = y.shape
-    _expect("weights", weights, (torch.float32,), (m, top))
-    _expect("dout", dout, (y.dtype,), (m, n))
-    _contiguous("positions", positions)
-    _contiguous("weights", weights)
-    dev = _device(dout=dout, y=y, weights=weights, positions=positions)
-    dy = torch.empty((rows, n), dtype=y.dtype, device=y.device)
-    dweights = torch.empty((m, top), dtype=torch.float32, device=y.device)
-    _check(_lib.pts_moe_combine_backward(dout.data_ptr(), _leading("dout", dout), y.data_ptr(), _DTYPES[y.dtype],
-                                         _leading("y", y), rows, weights.data_ptr(), positions.data_ptr(), m, n, top,
-                                         dy.data_ptr(), n, dweights.data_ptr(), _raw_stream(dev)))
+    _index("positions", positions, (m, top))
+    _weights("weights", weights, (m, top))
+    _exactly("dout", dout, y.dtype, (m, n))
+    dev, ld, ld_d = _device(y, dout, weights, positions), _leading("y", y), _leading("dout", dout)
+    dy = _empty((rows, n), (n, 1), dtype=y.dtype, device=y.device)
+    dweights = _empty((m, top), (top, 1), dtype=_F32, device=y.device)
+    status = _combine_backward(dout.data_ptr(), ld_d, y.data_ptr(), _DTYPES[y.dtype], ld, rows, weights.data_ptr(),
+                               positions.data_ptr(), m, n, top, dy.data_ptr(), n, dweights.data_ptr(), _raw_stream(dev))
+    if status:
+        _check(status)
     return dy, dweights
 
 
