@@ -32,7 +32,7 @@ template <bool BF16> struct Piece { // 16 bytes of a row
     __device__ __forceinline__ void load(const void *p, int64_t at, int valid, bool vec)
     {
         if (vec && valid >= N) {
-            const u32x4 w = *(const u32x4 *)((const uint8_t *)p + at * (BF16 ? 2 : 4));
+            const u32x4 w = __builtin_nontemporal_load((const u32x4 *)((const uint8_t *)p + at * (BF16 ? 2 : 4)));
             set(w);
             return;
         }
@@ -82,7 +82,9 @@ template <bool BF16> struct Piece { // 16 bytes of a row
     }
 };
 
-constexpr int COMBINE_UNROLL = 8; // rows in flight per thread
+// Rows in flight per thread. 8192 tokens x 8 rows x 4096, bf16: sum 99 us with 4
+// (6.1 TB/s), 109 with 8, 100 with 2; gradients 240, 245, 255 (4.8 TB/s).
+constexpr int COMBINE_UNROLL = 4;
 
 // One token's strip of 256 pieces per workgroup.
 template <bool BF16>

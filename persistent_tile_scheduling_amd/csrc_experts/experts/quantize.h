@@ -12,7 +12,7 @@
 // the maximum and the conversion.
 #pragma once
 
-#include "device/common.h"
+#include "lanes.h"
 
 namespace pts {
 
@@ -46,56 +46,70 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-// Eight values of one block to eight codes.
-__device__ __forceinline__ uint2 quantize8(const float (&x)[8], float s)
+// N (4 or 8) values of one block to codes, four to a word.
+template <int N> __device__ __forceinline__ void quantize(const float *x, float s, uint32_t (&out)[N / 4])
 {
-    float t[8];
+    float t[N];
     if (s >= 0x1p-60f) {
         const float r = 1.0f / s;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             t[i] = divide_by(x[i], s, r);
     } else { // tiny or NaN scales
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             t[i] = x[i] / s;
     }
-    return make_uint2(pack4(t[0], t[1], t[2], t[3]), pack4(t[4], t[5], t[6], t[7]));
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        out[i / 4] = pack4(t[i], t[i + 1], t[i + 2], t[i + 3]);
 }
 
-// Eight consecutive elements from p, of which the first `valid` exist; the rest
-// read as 0. VEC: p is 16-byte aligned.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const void *p, int valid, float (&x)[8])
+// A thread holds eight elements of a line of x as 16-byte pieces, one of bf16 or
+// two of fp32; the pieces of 16 (or 64) lanes side by side are what one load
+// instruction reads, so each uses the cache lines it touches whole. Element j
+// of the thread at place `at` of `lanes`:
+template <bool BF16> __device__ __forceinline__ constexpr int element(int at, int j, int lanes)
 {
-    if (VEC && valid >= 8) {
-        if constexpr (BF16) {
-            const u32x4 v = __builtin_nontemporal_load((const u32x4 *)p);
+    return BF16 ? at * 8 + j : j / 4 * lanes * 4 + at * 4 + j % 4;
+}
+
+// One piece from p, of which the first `valid` elements exist; the rest read as
+// 0. VEC: p is 16-byte aligned.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load_piece(const void *p, int valid, float *x)
+{
+    constexpr int N = BF16 ? 8 : 4;
+    if (VEC && valid >= N) {
+        const u32x4 v = __builtin_nontemporal_load((const u32x4 *)p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16) {
                 x[2 * i] = __uint_as_float(v[i] << 16);
                 x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-            }
-        } else {
-            const f32x4 v = __builtin_nontemporal_load((const f32x4 *)p);
-            const f32x4 w = __builtin_nontemporal_load((const f32x4 *)p + 1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = v[i];
-                x[4 + i] = w[i];
+            } else {
+                x[i] = __uint_as_float(v[i]);
             }
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
         x[i] = 0.f;
-        if (i < valid) {
-            if constexpr (BF16)
-                x[i] = __uint_as_float((uint32_t)((const uint16_t *)p)[i] << 16);
-            else
-                x[i] = ((const float *)p)[i];
-        }
+        if (i < valid)
+            x[i] = BF16 ? __uint_as_float((uint32_t)((const uint16_t *)p)[i] << 16) : ((const float *)p)[i];
+    }
+}
+
+// The thread's eight elements of a line that starts at p and has `valid`.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const uint8_t *p, int at, int lanes, int valid, float (&x)[8])
+{
+    constexpr int N = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
+#pragma unroll
+    for (int j = 0; j < 8; j += N) {
+        const int e = element<BF16>(at, j, lanes);
+        load_piece<BF16, VEC>(p + (int64_t)e * ES, valid - e, x + j);
     }
 }
 
@@ -110,54 +124,61 @@ struct QuantizeArgs {
     int32_t rows_per_group;   // rows one workgroup walks (row form)
 };
 
-// Maximum over the 16 lanes of a row of the wave, in every lane.
-__device__ __forceinline__ uint32_t max16(uint32_t v)
-{
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, false)); // rotate by 8
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xF, 0xF, false));
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x122, 0xF, 0xF, false));
-    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x121, 0xF, 0xF, false));
-    return v;
-}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 
 // Row form, x row-major: a wave reads 512 consecutive elements of a row (four
-// blocks, 16 lanes and 8 elements each), so a block's maximum stays inside a
-// DPP row. A workgroup walks `rows_per_group` rows of one 512-wide strip; the
-// strip's scales are collected in LDS and written together, since they are
-// stored with the rows next to each other (one k block's scales of
-// consecutive rows are what a product's tile reads).
+// blocks), so a block's maximum stays inside 16 lanes (bf16) or 32 (fp32). A
+// workgroup walks `rows_per_group` rows of one 512-wide strip; the strip's
+// scales are collected in LDS and written together, since they are stored with
+// the rows next to each other (one k block's scales of consecutive rows are
+// what a product's tile reads).
 template <bool BF16, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs args)
 {
+    constexpr int ES = BF16 ? 2 : 4, N = BF16 ? 8 : 4;
     __shared__ float scales[4][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int strip = blockIdx.x % args.strips, group = blockIdx.x / args.strips;
-    const int c = strip * 512 + lane * 8; // this lane's first column
+    const int c = strip * 512;
     const int valid = args.k - c, room = (args.k + 15) / 16 * 16 - c;
-    constexpr int ES = BF16 ? 2 : 4;
     const int row0 = group * args.rows_per_group;
     const int rows = min(args.rows_per_group, args.m - row0);
+#pragma unroll 2
     for (int r = wave; r < rows; r += 4) {
         const int64_t row = row0 + r;
         const uint8_t *p = (const uint8_t *)args.x + (row * args.ldx + c) * ES;
         float x[8];
-        load8<BF16, VEC>(p, valid, x);
+        load8<BF16, VEC>(p, lane, 64, valid, x);
         if constexpr (GATED) { // silu(gate) up; the reciprocal is good to 1 ulp, a division would take ten instructions
             float up[8];
-            load8<BF16, VEC>(p + (int64_t)args.k * ES, valid, up);
+            load8<BF16, VEC>(p + (int64_t)args.k * ES, lane, 64, valid, up);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 x[i] = x[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) * up[i];
         }
-        uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            most = max(most, abs_bits(x[i]));
-        const float s = block_scale(max16(most));
-        if (room > 0) // q's rows are padded to whole 16-byte pieces
-            *(uint2 *)(args.q + row * args.ldq + c) = quantize8(x, s);
-        if ((lane & 15) == 0)
-            scales[lane >> 4][r] = s;
+        for (int j = 0; j < 8; j += N) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                most = max(most, abs_bits(x[j + i]));
+            most = reduce_lanes<16>(most, larger);
+            if constexpr (!BF16)
+                most = reduce_step<16>(most, larger);
+            const float s = block_scale(most);
+            uint32_t codes[N / 4];
+            quantize<N>(x + j, s, codes);
+            const int e = element<BF16>(lane, j, 64);
+            if (e < room) { // q's rows are padded to whole 16-byte pieces
+                uint8_t *const q = args.q + row * args.ldq + c + e;
+                if constexpr (BF16)
+                    *(uint2 *)q = make_uint2(codes[0], codes[1]);
+                else
+                    *(uint32_t *)q = codes[0];
+            }
+            if (e % QBLOCK == 0)
+                scales[e / QBLOCK][r] = s;
+        }
     }
     __syncthreads();
     const int kb = strip * 4 + wave; // one wave per k block, lanes along the rows
@@ -166,23 +187,24 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
 }
 
 // Tile form: one 128 x 128 block of the output per workgroup, for x stored
-// column by column (COL; k-major input, codes still written row by row) and
-// for 128 x 128 scales. A thread holds an 8 x 8 piece in registers.
-//   row-major x: rows 8 a + i, columns 8 b .. 8 b + 7, a = tid / 16, b = tid % 16
-//   COL:         the same with the roles exchanged: 8 loads along the rows, each
-//                of 8 consecutive rows, then transposed on the way out through
-//                the order in which the piece is read.
-// Either way the codes leave through LDS, so that a row's 128 codes are
-// written as whole 16-byte pieces.
+// column by column (COL; the codes are still written row by row) and for
+// 128 x 128 scales. x's lines in memory (its rows, or with COL its columns) run
+// along the 16 lanes `fast`; a thread holds eight elements of each of eight
+// consecutive lines. The codes leave through LDS, so that a row's 128 codes are
+// written as whole 16-byte pieces; there, row r's sixteen 8-byte pieces are
+// exchanged by a number that follows the thread that writes them, which spreads
+// the 16 lanes' rows over the banks.
 template <bool BF16, bool COL, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs args)
 {
-    constexpr int ES = BF16 ? 2 : 4;
-    constexpr int PITCH = 144; // bytes per row of codes in LDS, a multiple of 16
+    constexpr int ES = BF16 ? 2 : 4, N = BF16 ? 8 : 4;
     __shared__ uint32_t most[QBLOCK];
-    __shared__ __align__(16) uint8_t codes[QBLOCK * PITCH];
+    __shared__ __align__(16) uint8_t codes[QBLOCK * QBLOCK];
+    auto place = [](int r, int piece) { // byte of 8-byte piece `piece` of row r
+        return r * QBLOCK + ((piece ^ ((COL ? r / N : r / 8) % 8 * 2)) * 8);
+    };
     const int tid = threadIdx.x;
-    const int fast = tid & 15, slow = tid >> 4;       // along the storage order of x, across it
+    const int fast = tid & 15, slow = tid >> 4;
     const int bk = blockIdx.x % args.strips, bm = blockIdx.x / args.strips;
     const int row0 = bm * QBLOCK, col0 = bk * QBLOCK;
     const int vm = min(QBLOCK, args.m - row0), vk = min(QBLOCK, args.k - col0);
@@ -194,8 +216,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int j = slow * 8 + i;
-        const uint8_t *p = (const uint8_t *)args.x + (base + (int64_t)j * args.ldx + fast * 8) * ES;
-        load8<BF16, VEC>(p, j < nslow ? nfast - fast * 8 : 0, x[i]);
+        load8<BF16, VEC>((const uint8_t *)args.x + (base + (int64_t)j * args.ldx) * ES, fast, 16, j < nslow ? nfast : 0,
+                         x[i]);
     }
     __syncthreads();
     if constexpr (SQUARE) {
@@ -205,8 +227,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs a
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v = max(v, abs_bits(x[i][j]));
-        v = max16(v);
-        if (fast == 0)
+        v = reduce_lanes<64>(v, larger);
+        if ((tid & 63) == 0)
             atomicMax(&most[0], v);
     } else { // COL: a row of the output is a fast index, its maximum runs over the slow ones
 #pragma unroll
@@ -215,26 +237,46 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs a
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v = max(v, abs_bits(x[i][j]));
-            atomicMax(&most[fast * 8 + j], v);
+            v = reduce_step<32>(reduce_step<16>(v, larger), larger); // the wave's four lines of lanes
+            if ((tid & 48) == 0)
+                atomicMax(&most[element<BF16>(fast, j, 16)], v);
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 8; ++r) { // the piece's output rows
-        float row[8];
+    for (int r = 0; r < 8; ++r) {
+        if constexpr (COL) { // transposed: eight consecutive k of one row
+            float row[8];
+            uint32_t out[2];
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-            row[t] = COL ? x[t][r] : x[r][t];
-        const int orow = (COL ? fast : slow) * 8 + r, ocol = (COL ? slow : fast) * 8;
-        *(uint2 *)(codes + orow * PITCH + ocol) = quantize8(row, block_scale(most[SQUARE ? 0 : orow]));
+            for (int t = 0; t < 8; ++t)
+                row[t] = x[t][r];
+            const int o = element<BF16>(fast, r, 16);
+            quantize<8>(row, block_scale(most[SQUARE ? 0 : o]), out);
+            *(uint2 *)(codes + place(o, slow)) = make_uint2(out[0], out[1]);
+        } else {
+            const int o = slow * 8 + r;
+            uint32_t out[2];
+            quantize<8>(x[r], block_scale(most[0]), out);
+            if constexpr (BF16) {
+                *(uint2 *)(codes + place(o, fast)) = make_uint2(out[0], out[1]);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = element<BF16>(fast, 4 * h, 16);
+                    *(uint32_t *)(codes + place(o, e / 8) + e % 8) = out[h];
+                }
+            }
+        }
     }
     __syncthreads();
     const int room = min(QBLOCK, (args.k + 15) / 16 * 16 - col0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = i * 32 + tid / 8, cc = (tid & 7) * 16;
-        if (r < vm && cc < room) // q's rows are padded to whole 16-byte pieces
-            *(u32x4 *)(args.q + (int64_t)(row0 + r) * args.ldq + col0 + cc) = *(const u32x4 *)(codes + r * PITCH + cc);
+        const int r = i * 32 + tid / 8, piece = (tid & 7) * 2;
+        if (r < vm && piece * 8 < room) // q's rows are padded to whole 16-byte pieces
+            *(u32x4 *)(args.q + (int64_t)(row0 + r) * args.ldq + col0 + piece * 8) =
+                *(const u32x4 *)(codes + place(r, piece));
     }
     if constexpr (SQUARE) {
         if (tid == 0)
