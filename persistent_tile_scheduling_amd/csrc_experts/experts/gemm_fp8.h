@@ -31,6 +31,7 @@ struct Fp8Args {
     int32_t m, n, k, nk;
     int32_t tiles_n, experts, a_rows;
     int32_t d_vec; // D's rows are 16-byte aligned
+    int32_t strip; // few rows: 16-column tiles per workgroup
 };
 
 // One row's share of a k block in a lane: lane l has, of row l % 16, the two
@@ -611,26 +612,31 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
     }
 }
 
-__device__ __forceinline__ i32x4 half(i32x8 v, int h) { return h ? i32x4{v[4], v[5], v[6], v[7]} : i32x4{v[0], v[1], v[2], v[3]}; }
-
 // ---- few rows ----------------------------------------------------------------
 
-// Up to 16 MB rows against 16 columns per workgroup, straight from memory to
-// registers: with so few rows every byte of B is used by one workgroup only, so
-// LDS would add a hop and a barrier. The eight waves take the k blocks in turn
-// (wave w: w, w + 8, ...), which gives 4096-deep weights eight independent
-// streams of loads per column strip, and their partial sums are added in wave
-// order through LDS at the end. Memory bound, so the codes are always widened.
-template <int MB, bool ROWS, bool BF16>
+// Up to 16 MB rows against a strip of 16-column tiles per workgroup, straight
+// from memory to registers: with so few rows every byte of B is used by one
+// workgroup only, so LDS would add a hop and a barrier. The eight waves take the
+// k blocks in turn (wave w: w, w + 8, ...), eight independent streams of loads,
+// and their partial sums are added in wave order through LDS for each tile; the
+// waves go on to the next tile's loads meanwhile.
+//
+// Memory bound: what counts is how many bytes are on their way. U k blocks per
+// wave at once: 4 where a compute unit has one or two workgroups (8 x 4096 x
+// 4096: 7 us), 2 where it can have four (59 registers; 128 rows over 55 of 64
+// experts, 4096 x 4096 each, 922 MB: 168 us, 5.5 TB/s, against 185 with 4). Two
+// tiles per workgroup there spare half the searches for the tile (one: 174 us;
+// eight: 179, too few workgroups to even out).
+template <int MB, int U, bool ROWS, bool BF16>
 __global__ __launch_bounds__(512) void gemm_fp8_rows_kernel(const Fp8Args args)
 {
-    constexpr int WAVES = 8, UNROLL = MB == 1 ? 4 : 2;
-    __shared__ __align__(16) float part[WAVES][MB * 16][16];
+    constexpr int WAVES = 8;
+    __shared__ __align__(16) float part[2][WAVES][MB * 16][16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
     Fp8Tile tile;
-    if (!fp8_find_tile(args, MB * 16, 16, blockIdx.x, tile))
+    if (!fp8_find_tile(args, MB * 16, 16 * args.strip, blockIdx.x, tile))
         return;
     const uint8_t *ap[MB];
     const float *sap[MB];
@@ -640,93 +646,101 @@ __global__ __launch_bounds__(512) void gemm_fp8_rows_kernel(const Fp8Args args)
         ap[i] = args.a + (int64_t)row * args.lda;
         sap[i] = args.sa + (int64_t)row * args.sa_m;
     }
-    const uint8_t *bp = args.b + tile.expert * args.b_expert + (int64_t)(tile.col0 + min(l16, tile.vn - 1)) * args.ldb;
-    const float *sbp = args.sb + tile.expert * args.sb_expert;
-    const int c4 = tile.col0 + g * 4; // the four columns this lane's results belong to
-    f32x4 acc[MB];
+    const uint8_t *const b = args.b + tile.expert * args.b_expert;
+    const float *const sbp = args.sb + tile.expert * args.sb_expert;
+    const int tiles = (tile.vn + 15) / 16;
+    for (int t = 0; t < tiles; ++t) {
+        const int col0 = tile.col0 + t * 16;
+        const uint8_t *const bp = b + (int64_t)min(col0 + l16, args.n - 1) * args.ldb;
+        f32x4 acc[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = wave; k0 < args.nk; k0 += WAVES * UNROLL) {
-        i32x8 b[UNROLL], a[UNROLL][MB];
-        float sa[UNROLL][MB];
-        f32x4 sb[UNROLL];
+        for (int i = 0; i < MB; ++i)
+            acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int k0 = wave; k0 < args.nk; k0 += WAVES * U) {
+            i32x4 x[U][2], y[U][MB][2];
+            float sa[U][MB], sb[U][ROWS ? 4 : 1];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int kb = min(k0 + u * WAVES, args.nk - 1); // past the end: read again, not used
-            const int last = min(7, (args.k - kb * 128 - 1) / 16);
-            const int64_t lo = (int64_t)kb * 128 + min(g, last) * 16, hi = (int64_t)kb * 128 + min(g + 4, last) * 16;
-            b[u] = __builtin_shufflevector(*(const i32x4 *)(bp + lo), *(const i32x4 *)(bp + hi), 0, 1, 2, 3, 4, 5, 6, 7);
+            for (int u = 0; u < U; ++u) {
+                const int kb = min(k0 + u * WAVES, args.nk - 1); // past the end: read again, not used
+                const int last = min(7, (args.k - kb * 128 - 1) / 16);
+                const int64_t lo = (int64_t)kb * 128 + min(g, last) * 16, hi = (int64_t)kb * 128 + min(g + 4, last) * 16;
+                x[u][0] = *(const i32x4 *)(bp + lo);
+                x[u][1] = *(const i32x4 *)(bp + hi);
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                a[u][i] = __builtin_shufflevector(*(const i32x4 *)(ap[i] + lo), *(const i32x4 *)(ap[i] + hi), 0, 1, 2, 3,
-                                                  4, 5, 6, 7);
-                sa[u][i] = sap[i][kb * args.sa_k];
+                for (int i = 0; i < MB; ++i) {
+                    y[u][i][0] = *(const i32x4 *)(ap[i] + lo);
+                    y[u][i][1] = *(const i32x4 *)(ap[i] + hi);
+                    sa[u][i] = sap[i][kb * args.sa_k];
+                }
+#pragma unroll
+                for (int r = 0; r < (ROWS ? 4 : 1); ++r)
+                    sb[u][r] = sbp[(ROWS ? min(col0 + g * 4 + r, args.n - 1) : col0 >> 7) * args.sb_n + kb * args.sb_k];
             }
-            if constexpr (ROWS) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sb[u][r] = sbp[min(c4 + r, args.n - 1) * args.sb_n + kb * args.sb_k];
-            } else {
-                const float s = sbp[(tile.col0 >> 7) * args.sb_n + kb * args.sb_k];
-                sb[u] = f32x4{s, s, s, s};
-            }
-        }
+            for (int u = 0; u < U; ++u) {
+                const int kb = k0 + u * WAVES;
+                if (kb >= args.nk)
+                    break;
+                const int left = args.k - kb * 128;
+                if (left < 128) { // bytes past the end of the rows are cleared in both operands
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int kb = k0 + u * WAVES;
-            if (kb >= args.nk)
-                break;
-            const int left = args.k - kb * 128;
-            if (left < 128) { // bytes past the end of the rows are cleared in both operands
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const int at = (w < 4 ? g : g + 4) * 16 + (w & 3) * 4;
-                    const int bytes = min(max(left - at, 0), 4);
-                    const int mask = bytes == 4 ? -1 : (int)((1u << (8 * bytes)) - 1u);
-                    b[u][w] &= mask;
+                        for (int w = 0; w < 4; ++w) {
+                            const int bytes = min(max(left - (g + 4 * h) * 16 - w * 4, 0), 4);
+                            const int mask = bytes == 4 ? -1 : (int)((1u << (8 * bytes)) - 1u);
+                            x[u][h][w] &= mask;
 #pragma unroll
-                    for (int i = 0; i < MB; ++i)
-                        a[u][i][w] &= mask;
+                            for (int i = 0; i < MB; ++i)
+                                y[u][i][h][w] &= mask;
+                        }
+                }
+                Fragment<!BF16> fx;
+                fx.set(x[u][0], x[u][1]);
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    Fragment<!BF16> fy;
+                    fy.set(y[u][i][0], y[u][i][1]);
+                    const f32x4 p = block_sums(fx, fy);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][r] = fmaf(p[r], sa[u][i] * sb[u][ROWS ? r : 0], acc[i][r]);
                 }
             }
-            Fragment<true> x;
-            x.set(half(b[u], 0), half(b[u], 1));
+        }
+        float (*const sums)[MB * 16][16] = part[t & 1];
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                Fragment<true> y;
-                y.set(half(a[u][i], 0), half(a[u][i], 1));
-                const f32x4 p = block_sums(x, y);
+        for (int i = 0; i < MB; ++i)
+            *(f32x4 *)&sums[wave][i * 16 + l16][g * 4] = acc[i];
+        barrier_lds(); // tile t - 1 was added up before this, so its half may be written next
+        if (tid < MB * 64) {
+            const int r = tid >> 2, c = (tid & 3) * 4;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[i][r] = fmaf(p[r], sa[u][i] * sb[u][r], acc[i][r]);
+            for (int w = 0; w < WAVES; ++w) {
+                const f32x4 p = *(const f32x4 *)&sums[w][r][c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] += p[i];
+            }
+            const int valid = tile.vn - t * 16 - c;
+            if (r < tile.vm) {
+                const int64_t at = (int64_t)(tile.row0 + r) * args.ldd + col0 + c;
+                if constexpr (BF16) {
+                    if (args.d_vec && valid >= 4) {
+                        const bf16x4 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+                        *(bf16x4 *)((__bf16 *)args.d + at) = h;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < valid)
+                                ((__bf16 *)args.d)[at + i] = (__bf16)v[i];
+                    }
+                } else {
+                    fp8_store_row<false, 4>(args.d, at, v, valid, args.d_vec);
+                }
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-        *(f32x4 *)&part[wave][i * 16 + l16][g * 4] = acc[i];
-    __syncthreads();
-    if (tid < MB * 64) {
-        const int r = tid >> 2, c = (tid & 3) * 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const f32x4 p = *(const f32x4 *)&part[w][r][c];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] += p[i];
-        }
-        if (r < tile.vm)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c + i < tile.vn) {
-                    const int64_t at = (int64_t)(tile.row0 + r) * args.ldd + tile.col0 + c + i;
-                    if constexpr (BF16)
-                        ((__bf16 *)args.d)[at] = (__bf16)v[i];
-                    else
-                        ((float *)args.d)[at] = v[i];
-                }
     }
 }
 

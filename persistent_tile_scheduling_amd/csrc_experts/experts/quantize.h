@@ -9,7 +9,8 @@
 //
 // Memory bound: 2 or 4 bytes read (twice that with the gate) and 1 byte
 // written per element; each element is read once and kept in registers between
-// the maximum and the conversion.
+// the maximum and the conversion. (Loads are ordinary ones: rows need not start
+// at a cache line, and a streaming load would fetch the shared lines twice.)
 #pragma once
 
 #include "lanes.h"
@@ -81,7 +82,7 @@ __device__ __forceinline__ void load_piece(const void *p, int valid, float *x)
 {
     constexpr int N = BF16 ? 8 : 4;
     if (VEC && valid >= N) {
-        const u32x4 v = __builtin_nontemporal_load((const u32x4 *)p);
+        const u32x4 v = *(const u32x4 *)p;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (BF16) {
@@ -131,7 +132,8 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(
 // workgroup walks `rows_per_group` rows of one 512-wide strip; the strip's
 // scales are collected in LDS and written together, since they are stored with
 // the rows next to each other (one k block's scales of consecutive rows are
-// what a product's tile reads).
+// what a product's tile reads). 8192 x 7000 with the gate, bf16: 55 us (5.3
+// TB/s, a large copy's rate) with 8 rows per workgroup, 59 with 4 or 32.
 template <bool BF16, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs args)
 {
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
 // consecutive lines. The codes leave through LDS, so that a row's 128 codes are
 // written as whole 16-byte pieces; there, row r's sixteen 8-byte pieces are
 // exchanged by a number that follows the thread that writes them, which spreads
-// the 16 lanes' rows over the banks.
+// the 16 lanes' rows over the banks. 5000 x 7000 fp32 by columns: 36 us (4.9 TB/s).
 template <bool BF16, bool COL, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs args)
 {

@@ -65,15 +65,6 @@ bool in_range(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
 // ---- products ------------------------------------------------------------------
 
-template <int MB> gemm_status launch_rows(pts::Fp8Args &args, bool rows, bool bf16, int64_t tiles_m, void *stream)
-{
-    args.tiles_n = (int32_t)ceil_div(args.n, 16);
-    void (*k)(pts::Fp8Args) =
-        rows ? (bf16 ? &pts::gemm_fp8_rows_kernel<MB, true, true> : &pts::gemm_fp8_rows_kernel<MB, true, false>)
-             : (bf16 ? &pts::gemm_fp8_rows_kernel<MB, false, true> : &pts::gemm_fp8_rows_kernel<MB, false, false>);
-    return launch_blocks(k, tiles_m * args.tiles_n, 512, args, stream);
-}
-
 // Tile rows of height bm: exact for one product; for experts the most there can
 // be, since each expert with rows adds at most one partial tile.
 int64_t tile_rows(const pts::Fp8Args &args, int64_t bm)
@@ -81,6 +72,28 @@ int64_t tile_rows(const pts::Fp8Args &args, int64_t bm)
     if (args.offsets == nullptr)
         return ceil_div(args.m, bm);
     return (args.m + std::min<int64_t>(args.experts, args.m) * (bm - 1)) / bm;
+}
+
+template <int MB, int U> gemm_status launch_rows_kernel(pts::Fp8Args &args, bool rows, bool bf16, int64_t blocks, void *stream)
+{
+    void (*k)(pts::Fp8Args) =
+        rows ? (bf16 ? &pts::gemm_fp8_rows_kernel<MB, U, true, true> : &pts::gemm_fp8_rows_kernel<MB, U, true, false>)
+             : (bf16 ? &pts::gemm_fp8_rows_kernel<MB, U, false, true> : &pts::gemm_fp8_rows_kernel<MB, U, false, false>);
+    return launch_blocks(k, blocks, 512, args, stream);
+}
+
+// Few rows, 16-column tiles: two per workgroup where there are plenty, and
+// fewer loads in flight per wave where several workgroups share a compute unit
+// (measured at the kernel).
+template <int MB> gemm_status launch_rows(pts::Fp8Args &args, bool rows, bool bf16, int cus, void *stream)
+{
+    const int64_t tiles_m = tile_rows(args, 16 * MB), tiles = tiles_m * ceil_div(args.n, 16);
+    args.strip = tiles >= 16 * (int64_t)cus ? 2 : 1;
+    args.tiles_n = (int32_t)ceil_div(args.n, 16 * args.strip);
+    if constexpr (MB == 1)
+        if (tiles <= 2 * (int64_t)cus)
+            return launch_rows_kernel<1, 4>(args, rows, bf16, tiles, stream);
+    return launch_rows_kernel<MB, 2>(args, rows, bf16, tiles_m * args.tiles_n, stream);
 }
 
 template <class C> gemm_status launch_tiles(pts::Fp8Args &args, int cus, void *stream)
@@ -113,11 +126,11 @@ gemm_status run_product(pts::Fp8Args &args, bool rows, bool bf16, void *stream)
     if (tile_rows(args, 16) * ceil_div(args.n, 16) > INT32_MAX)
         return fail(GEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
     if (together <= 16)
-        return launch_rows<1>(args, rows, bf16, tile_rows(args, 16), stream);
+        return launch_rows<1>(args, rows, bf16, cus, stream);
     if (together <= 32)
-        return launch_rows<2>(args, rows, bf16, tile_rows(args, 32), stream);
+        return launch_rows<2>(args, rows, bf16, cus, stream);
     if (together <= 64)
-        return launch_rows<4>(args, rows, bf16, tile_rows(args, 64), stream);
+        return launch_rows<4>(args, rows, bf16, cus, stream);
     if (rows)
         return bf16 ? run_tiles<true, true>(args, together, cus, stream) : run_tiles<true, false>(args, together, cus, stream);
     return bf16 ? run_tiles<false, true>(args, together, cus, stream) : run_tiles<false, false>(args, together, cus, stream);
@@ -238,11 +251,9 @@ gemm_status pts_quantize_fp8(const void *x, int32_t dtype_x, int32_t layout_x, i
         const gemm_status st = compute_units(&cus);
         if (st != GEMM_OK)
             return st;
-        // up to 64 rows per workgroup, fewer while that would leave compute units idle
+        // 8 rows per workgroup, 4 (one per wave) while 8 would leave compute units idle
         const int64_t strips = ceil_div(k, 512);
-        int64_t per = 64;
-        while (per > 4 && ceil_div(m, per) * strips < 4 * (int64_t)cus)
-            per /= 2;
+        const int64_t per = ceil_div(m, 8) * strips < 4 * (int64_t)cus ? 4 : 8;
         args.rows_per_group = (int32_t)per;
         args.strips = (int32_t)strips;
         void (*kern)(pts::QuantizeArgs);
@@ -279,7 +290,7 @@ gemm_status pts_gemm_fp8(const void *a, int64_t lda, const float *a_scale, int64
         return st;
     pts::Fp8Args args{(const uint8_t *)a, (const uint8_t *)b, a_scale, b_scale, d, nullptr, nullptr, lda, ldb, ldd,
                       s.a_m, s.a_k, s.b_n, s.b_k, 0, 0, (int32_t)m, (int32_t)n, (int32_t)k,
-                      (int32_t)ceil_div(k, PTS_FP8_BLOCK), 0, 1, (int32_t)m, vector_rows(d, ldd, dtype_d)};
+                      (int32_t)ceil_div(k, PTS_FP8_BLOCK), 0, 1, (int32_t)m, vector_rows(d, ldd, dtype_d), 1};
     return run_product(args, b_block_n == 1, dtype_d == GEMM_DTYPE_BF16, stream);
 }
 
@@ -306,7 +317,7 @@ gemm_status pts_gemm_fp8_experts(const void *a, int64_t a_rows, int64_t lda, con
     pts::Fp8Args args{(const uint8_t *)a, (const uint8_t *)b, a_scale, b_scale, d, offsets, rows, lda, ldb, ldd,
                       s.a_m, s.a_k, s.b_n, s.b_k, b_stride_expert, b_scale_stride_expert, (int32_t)m, (int32_t)n,
                       (int32_t)k, (int32_t)ceil_div(k, PTS_FP8_BLOCK), 0, experts, (int32_t)a_rows,
-                      vector_rows(d, ldd, dtype_d)};
+                      vector_rows(d, ldd, dtype_d), 1};
     return run_product(args, false, dtype_d == GEMM_DTYPE_BF16, stream);
 }
 
