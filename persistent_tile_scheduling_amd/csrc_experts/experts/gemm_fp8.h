@@ -224,20 +224,21 @@ __device__ __forceinline__ void fp8_store_row(void *d, int64_t at, const float (
 
 // ---- tiles through LDS -------------------------------------------------------
 
-// WM_ x WN_ waves, each a (BM / WM_) x (BN / WN_) piece. ROWS: B's scales are
-// per row of 128 k (as A's), otherwise per 128 x 128.
-template <int BM_, int BN_, int WM_, int WN_, bool ROWS_, bool BF16_>
+// WM_ x WN_ waves, each a (BM / WM_) x (BN / WN_) piece; a ring of STAGES_ k
+// blocks. ROWS: B's scales are per row of 128 k (as A's), otherwise per 128 x 128.
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool ROWS_, bool BF16_>
 struct Fp8Config {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WAVES = WM * WN, THREADS = 64 * WAVES;
     static constexpr bool ROWS = ROWS_, BF16 = BF16_, EXACT = !BF16_;
     static constexpr int WTM = BM / WM, WTN = BN / WN, MI = WTM / 16, NI = WTN / 16;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-    static constexpr int S_BYTES = (BM + BN) * 4;
+    static constexpr int STAGES = STAGES_;
+    static constexpr int S_BYTES = THREADS * 4; // one scale per thread, past BM + BN a copy
     static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
     static constexpr int LOADS_A = A_BYTES / 16 / THREADS, LOADS_B = B_BYTES / 16 / THREADS;
     static_assert(BM + BN <= THREADS && BM % 64 == 0 && BN % 64 == 0, "one scale per thread and stage");
     static_assert(NI == 4 && 128 % WTN == 0, "a wave's columns share a block scale, 16 per lane");
-    static_assert(2 * STAGE <= 160 * 1024, "two stages");
+    static_assert(STAGES >= 2 && STAGES * STAGE <= 160 * 1024 && (STAGES - 2) * (LOADS_A + LOADS_B + 1) <= 63, "ring");
 };
 
 template <class C>
@@ -274,14 +275,12 @@ struct Fp8Loop {
             const int r = (wave * C::LOADS_B + i) * 8 + lane / 8;
             b_off[i] = (uint32_t)min(r, t.vn - 1) * (uint32_t)args.ldb + (((lane & 7) ^ swizzle_b(r)) << 4);
         }
-        s_off = s_step = 0;
-        s_rsrc = a_rsrc;
         if (wave * 64 < C::BM) {
             const int row = fp8_a_row(args, t.row0 + min(wave * 64 + lane, t.vm - 1)) - (int)first;
             s_rsrc = buffer_rsrc(args.sa + first * args.sa_m);
             s_off = (uint32_t)row * (uint32_t)args.sa_m * 4u;
             s_step = (uint32_t)args.sa_k * 4u;
-        } else if (wave * 64 < C::BM + C::BN) {
+        } else {
             const int col = t.col0 + min(wave * 64 + lane - C::BM, t.vn - 1);
             s_rsrc = buffer_rsrc(args.sb + t.expert * args.sb_expert);
             s_off = (uint32_t)(C::ROWS ? col : col >> 7) * (uint32_t)args.sb_n * 4u;
@@ -321,8 +320,7 @@ struct Fp8Loop {
                                b_off[i] - ((c > last ? c - last : 0u) << 4), b_rsrc, at);
             }
         }
-        if (C::BM + C::BN == C::THREADS || wave * 64 < C::BM + C::BN)
-            dma_load4(stage + C::A_BYTES + C::B_BYTES + wave * 256, s_off, s_rsrc, (uint32_t)kb * s_step);
+        dma_load4(stage + C::A_BYTES + C::B_BYTES + wave * 256, s_off, s_rsrc, (uint32_t)kb * s_step);
     }
 
     // Load I of the PIECES that `issue` starts, for a whole k block.
@@ -335,7 +333,7 @@ struct Fp8Loop {
         else if constexpr (I < C::LOADS_A + C::LOADS_B)
             dma_load16_imm(stage + wave * (C::LOADS_B * 1024), C::A_BYTES + (I - C::LOADS_A) * 1024, b_off[I - C::LOADS_A],
                            b_rsrc, at);
-        else if (C::BM + C::BN == C::THREADS || wave * 64 < C::BM + C::BN)
+        else
             dma_load4(stage + C::A_BYTES + C::B_BYTES + wave * 256, s_off, s_rsrc, (uint32_t)kb * s_step);
     }
 
@@ -485,7 +483,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
 {
     using Loop = Fp8Loop<C>;
     using Wave = Fp8Wave<C>;
-    __shared__ __align__(1024) uint8_t smem[2 * C::STAGE];
+    __shared__ __align__(1024) uint8_t smem[C::STAGES * C::STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
@@ -511,29 +509,36 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
         };
         // One k block. LAST: none follows. Otherwise the next one's stage is
         // taken over on the way, before the last row of blocks, and the loads of
-        // the block after that are started. STEADY: that one is whole, and its
-        // loads are started one by one between the matrix instructions from
-        // there into the next block (all at once they hold up every wave: 8192^3
-        // 520 us against 480); `pending` says that the block before did so.
+        // the block STAGES further on go into the stage handed back. STEADY:
+        // that one is whole, and its loads are started one by one between the
+        // matrix instructions from there into the next block (all at once they
+        // hold up every wave: 8192^3 520 us against 480); `pending` says that
+        // the block before did so.
         bool pending = false;
+        uint32_t here = 0; // the block's stage, byte offset
+        auto after = [](uint32_t stage) { return stage + C::STAGE == C::STAGES * C::STAGE ? 0u : stage + C::STAGE; };
         auto k_block = [&](int kb, auto kind) {
             constexpr bool MORE = kind.value != LAST, IN_STEPS = kind.value == STEADY;
-            constexpr int HANDOVER = Wave::STEPS - C::NI / Wave::STEP, PER_STEP = C::EXACT ? 2 : 1;
+            constexpr int HANDOVER = Wave::STEPS - C::NI / Wave::STEP, PER_STEP = C::EXACT ? 2 : Loop::PIECES > Wave::STEPS ? 2 : 1;
             static_assert((Loop::PIECES + PER_STEP - 1) / PER_STEP <= Wave::STEPS, "started before the stage is waited for");
-            const uint32_t here = (kb & 1) * C::STAGE, there = C::STAGE - here;
+            const uint32_t before = here == 0 ? (C::STAGES - 1) * C::STAGE : here - C::STAGE;
             const uint8_t *const stage = smem + here;
-            uint8_t *const next = smem + there;
+            uint8_t *const next = smem + after(here);
             static_for<Wave::STEPS>([&](auto n) {
                 constexpr int N = n.value, I = N * Wave::STEP / C::NI, J = N * Wave::STEP % C::NI;
                 if constexpr (J == 0 && I + 1 < C::MI)
                     w.load_a((I + 1) & 1, I + 1, stage);
                 if constexpr (J == 0 && I + 1 == C::MI && MORE) {
-                    // Everything this wave needs of the stage is in registers: hand it back, take the next one.
-                    wait_vmcnt<0>();
+                    // Everything this wave needs of the stage is in registers: hand it back, take the next one. Of the
+                    // loads started, the ones of the STAGES - 2 blocks after that may still be on their way.
+                    if (kb + C::STAGES - 1 < args.nk)
+                        wait_vmcnt<(C::STAGES - 2) * Loop::PIECES>();
+                    else
+                        wait_vmcnt<0>();
                     barrier_lds();
                     if constexpr (!IN_STEPS) {
-                        if (kb + 2 < args.nk)
-                            loop.issue(lds + here, kb + 2, args.k);
+                        if (kb + C::STAGES < args.nk)
+                            loop.issue(lds + here, kb + C::STAGES, args.k);
                         enter(next, kb + 1);
                     }
                     w.load_a((I + 1) & 1, 0, next);
@@ -542,14 +547,14 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
                 keep_order();
                 static_for<PER_STEP>([&](auto u) {
                     if constexpr (N >= HANDOVER && IN_STEPS) {
-                        constexpr int I = (N - HANDOVER) * PER_STEP + u.value;
-                        if constexpr (I < Loop::PIECES)
-                            loop.template issue_piece<I>(lds + here, kb + 2);
+                        constexpr int P = (N - HANDOVER) * PER_STEP + u.value;
+                        if constexpr (P < Loop::PIECES)
+                            loop.template issue_piece<P>(lds + here, kb + C::STAGES);
                     } else if constexpr (N < HANDOVER && MORE) {
-                        constexpr int I = (N + Wave::STEPS - HANDOVER) * PER_STEP + u.value;
-                        if constexpr (I < Loop::PIECES)
+                        constexpr int P = (N + Wave::STEPS - HANDOVER) * PER_STEP + u.value;
+                        if constexpr (P < Loop::PIECES)
                             if (pending)
-                                loop.template issue_piece<I>(lds + there, kb + 1);
+                                loop.template issue_piece<P>(lds + before, kb - 1 + C::STAGES);
                     }
                 });
                 w.template add<N - Wave::LAG>();
@@ -567,13 +572,18 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
                     static_for<C::NI>([&](auto j) { w.load_col(j.value, next); });
                 }
             }
+            here = after(here);
         };
         if (args.nk > 0) {
-            loop.issue(lds, 0, args.k);
-            wait_vmcnt<0>();
+            for (int kb = 0; kb < min(C::STAGES - 1, args.nk); ++kb)
+                loop.issue(lds + kb * C::STAGE, kb, args.k);
+            if (args.nk >= C::STAGES - 1)
+                wait_vmcnt<(C::STAGES - 2) * Loop::PIECES>();
+            else
+                wait_vmcnt<0>();
             barrier_lds();
-            if (args.nk > 1)
-                loop.issue(lds + C::STAGE, 1, args.k);
+            if (args.nk > C::STAGES - 1)
+                loop.issue(lds + (C::STAGES - 1) * C::STAGE, C::STAGES - 1, args.k);
             enter(smem, 0);
 #pragma unroll
             for (int j = 0; j < C::NI; ++j) {
@@ -584,7 +594,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
             w.load_scales(smem);
             const int whole = args.k / 128;
             int kb = 0;
-            for (; kb + 2 < whole; ++kb) {
+            for (; kb + C::STAGES < whole; ++kb) {
                 k_block(kb, IntC<STEADY>{});
                 pending = true;
             }
@@ -592,7 +602,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
                 k_block(kb, IntC<GENERAL>{});
                 pending = false;
             }
-            k_block(kb, IntC<LAST>{});
+            k_block(args.nk - 1, IntC<LAST>{});
         }
         const int col0 = wn * C::WTN + (lane >> 4) * 16;
 #pragma unroll

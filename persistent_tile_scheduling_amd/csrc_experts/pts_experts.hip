@@ -74,63 +74,85 @@ int64_t tile_rows(const pts::Fp8Args &args, int64_t bm)
     return (args.m + std::min<int64_t>(args.experts, args.m) * (bm - 1)) / bm;
 }
 
-template <int MB, int U> gemm_status launch_rows_kernel(pts::Fp8Args &args, bool rows, bool bf16, int64_t blocks, void *stream)
-{
-    void (*k)(pts::Fp8Args) =
-        rows ? (bf16 ? &pts::gemm_fp8_rows_kernel<MB, U, true, true> : &pts::gemm_fp8_rows_kernel<MB, U, true, false>)
-             : (bf16 ? &pts::gemm_fp8_rows_kernel<MB, U, false, true> : &pts::gemm_fp8_rows_kernel<MB, U, false, false>);
-    return launch_blocks(k, blocks, 512, args, stream);
-}
-
 // Few rows, 16-column tiles: two per workgroup where there are plenty, and
 // fewer loads in flight per wave where several workgroups share a compute unit
 // (measured at the kernel).
+template <int MB, int U, bool ROWS, bool BF16> gemm_status launch_rows_kernel(pts::Fp8Args &args, int cus, void *stream)
+{
+    const int64_t tiles_m = tile_rows(args, 16 * MB);
+    args.strip = tiles_m * ceil_div(args.n, 16) >= 16 * (int64_t)cus ? 2 : 1;
+    args.tiles_n = (int32_t)ceil_div(args.n, 16 * args.strip);
+    return launch_blocks(&pts::gemm_fp8_rows_kernel<MB, U, ROWS, BF16>, tiles_m * args.tiles_n, 512, args, stream);
+}
+
+template <int MB, bool ROWS, bool BF16> gemm_status launch_rows_typed(pts::Fp8Args &args, int cus, void *stream)
+{
+    if constexpr (MB == 1)
+        if (tile_rows(args, 16) * ceil_div(args.n, 16) <= 2 * (int64_t)cus)
+            return launch_rows_kernel<1, 4, ROWS, BF16>(args, cus, stream);
+    return launch_rows_kernel<MB, 2, ROWS, BF16>(args, cus, stream);
+}
+
 template <int MB> gemm_status launch_rows(pts::Fp8Args &args, bool rows, bool bf16, int cus, void *stream)
 {
-    const int64_t tiles_m = tile_rows(args, 16 * MB), tiles = tiles_m * ceil_div(args.n, 16);
-    args.strip = tiles >= 16 * (int64_t)cus ? 2 : 1;
-    args.tiles_n = (int32_t)ceil_div(args.n, 16 * args.strip);
-    if constexpr (MB == 1)
-        if (tiles <= 2 * (int64_t)cus)
-            return launch_rows_kernel<1, 4>(args, rows, bf16, tiles, stream);
-    return launch_rows_kernel<MB, 2>(args, rows, bf16, tiles_m * args.tiles_n, stream);
+    if (rows)
+        return bf16 ? launch_rows_typed<MB, true, true>(args, cus, stream) : launch_rows_typed<MB, true, false>(args, cus, stream);
+    return bf16 ? launch_rows_typed<MB, false, true>(args, cus, stream) : launch_rows_typed<MB, false, false>(args, cus, stream);
 }
 
 template <class C> gemm_status launch_tiles(pts::Fp8Args &args, int cus, void *stream)
 {
     args.tiles_n = (int32_t)ceil_div(args.n, C::BN);
-    const int64_t resident = (int64_t)cus * (160 * 1024 / (2 * C::STAGE));
+    const int64_t resident = (int64_t)cus * (160 * 1024 / (C::STAGES * C::STAGE));
     return launch_blocks(&pts::gemm_fp8_tile_kernel<C>, std::min(tile_rows(args, C::BM) * args.tiles_n, resident), C::THREADS,
                          args, stream);
 }
 
-// The tile of a product with more than 64 rows together: the large one once its
-// tiles reach 55% of the compute units and the rows fill it.
+// The kernel of a product, by its output type, the rows that share a weight
+// (`together`: all of them, or the experts' average) and the number of tiles.
+// Times in us on MI355X, m x n x k.
+//
+// 256 x 256 tiles (bf16 results) once they reach 55% of the compute units:
+// 2048 x 8192 x 8192 128 against 141 with 128 x 128; 2048 x 4096 x 4096 (half of
+// the units) 41 with 128 x 128. Experts need more than 192 rows each (64
+// experts, 4096 x 4096: 224 rows 389 against 425, 160 rows 128 x 128: 334). For
+// fp32 results, whose widened operands keep the vector units busy, 128 x 128 is
+// as good or better throughout (4096 x 8192 x 8192: 603 against 665 with 256 x
+// 128), two independent workgroups per compute unit hiding each other's waits.
+//
+// 64 x 128 tiles while 128 x 128 ones would not outnumber the compute units
+// (1024 x 4096 x 4096: 24 against 31; 768 x 8192 x 8192: 64 against 59), and for
+// experts of up to 64 rows.
 template <bool ROWS, bool BF16> gemm_status run_tiles(pts::Fp8Args &args, int64_t together, int cus, void *stream)
 {
-    constexpr int BN = BF16 ? 256 : 128; // widened fragments take twice the registers: half the columns
-    const int64_t big = tile_rows(args, 256) * ceil_div(args.n, BN);
-    if (20 * big >= 11 * (int64_t)cus && together > 192)
-        return launch_tiles<pts::Fp8Config<256, BN, BF16 ? 2 : 4, BF16 ? 4 : 2, ROWS, BF16>>(args, cus, stream);
-    return launch_tiles<pts::Fp8Config<128, 128, 2, 2, ROWS, BF16>>(args, cus, stream);
+    if constexpr (BF16)
+        if (together > 192 && 20 * tile_rows(args, 256) * ceil_div(args.n, 256) >= 11 * (int64_t)cus)
+            return launch_tiles<pts::Fp8Config<256, 256, 2, 4, 2, ROWS, true>>(args, cus, stream);
+    if (together > 64 && tile_rows(args, 128) * ceil_div(args.n, 128) > cus)
+        return launch_tiles<pts::Fp8Config<128, 128, 2, 2, 2, ROWS, BF16>>(args, cus, stream);
+    return launch_tiles<pts::Fp8Config<64, 128, 2, 2, 3, ROWS, BF16>>(args, cus, stream);
 }
 
+// The kernel without LDS up to 4 rows per expert (2 rows each 159 against 167
+// with 64 x 128 tiles, 8 rows 235 against 211), and for one product up to 32
+// rows, or 64 for fp32 results (32 x 4096 x 4096: 9.5 against 14.7; 64 rows bf16:
+// 13.1 and 14.9, 64 x 8192 x 8192: 43 and 26; fp32 14 and 29, 44 and 53).
 gemm_status run_product(pts::Fp8Args &args, bool rows, bool bf16, void *stream)
 {
     int cus = 0;
     gemm_status st = compute_units(&cus);
     if (st != GEMM_OK)
         return st;
-    // rows that share a weight: all, or the experts' average
-    const int64_t together = args.offsets == nullptr ? args.m : ceil_div(args.m, args.experts);
+    const bool one = args.offsets == nullptr;
+    const int64_t together = one ? args.m : ceil_div(args.m, args.experts);
     if (tile_rows(args, 16) * ceil_div(args.n, 16) > INT32_MAX)
         return fail(GEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
-    if (together <= 16)
+    if (together <= (one ? 16 : 4))
         return launch_rows<1>(args, rows, bf16, cus, stream);
-    if (together <= 32)
+    if (one && together <= 32)
         return launch_rows<2>(args, rows, bf16, cus, stream);
-    if (together <= 64)
-        return launch_rows<4>(args, rows, bf16, cus, stream);
+    if (one && together <= 64 && !bf16)
+        return rows ? launch_rows_kernel<4, 2, true, false>(args, cus, stream) : launch_rows_kernel<4, 2, false, false>(args, cus, stream);
     if (rows)
         return bf16 ? run_tiles<true, true>(args, together, cus, stream) : run_tiles<true, false>(args, together, cus, stream);
     return bf16 ? run_tiles<false, true>(args, together, cus, stream) : run_tiles<false, false>(args, together, cus, stream);
