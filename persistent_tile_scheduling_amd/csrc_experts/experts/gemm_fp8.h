@@ -574,6 +574,20 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
             }
             here = after(here);
         };
+        // A wave whose rows or columns all lie past the tile's edge only loads
+        // and meets the others: its partner on the SIMD has the matrix unit to itself.
+        auto k_block_idle = [&](int kb) {
+            if (kb + C::STAGES - 1 < args.nk)
+                wait_vmcnt<(C::STAGES - 2) * Loop::PIECES>();
+            else
+                wait_vmcnt<0>();
+            barrier_lds();
+            if (kb + C::STAGES < args.nk)
+                loop.issue(lds + here, kb + C::STAGES, args.k);
+            here = after(here);
+            enter(smem + here, kb + 1);
+        };
+        const bool idle = wm * C::WTM >= tile.vm || wn * C::WTN >= tile.vn;
         if (args.nk > 0) {
             for (int kb = 0; kb < min(C::STAGES - 1, args.nk); ++kb)
                 loop.issue(lds + kb * C::STAGE, kb, args.k);
@@ -585,6 +599,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
             if (args.nk > C::STAGES - 1)
                 loop.issue(lds + (C::STAGES - 1) * C::STAGE, C::STAGES - 1, args.k);
             enter(smem, 0);
+        }
+        if (idle) {
+            for (int kb = 0; kb + 1 < args.nk; ++kb)
+                k_block_idle(kb);
+        } else if (args.nk > 0) {
 #pragma unroll
             for (int j = 0; j < C::NI; ++j) {
                 w.load_b(j, smem);
