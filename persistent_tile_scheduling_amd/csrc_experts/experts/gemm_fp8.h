@@ -32,6 +32,7 @@ struct Fp8Args {
     int32_t tiles_n, experts, a_rows;
     int32_t d_vec; // D's rows are 16-byte aligned
     int32_t strip; // few rows: 16-column tiles per workgroup
+    int32_t round; // tiles: the width of the dealing to the dies
 };
 
 // One row's share of a k block in a lane: lane l has, of row l % 16, the two
@@ -493,7 +494,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
     const uint32_t lds = lds_address(smem);
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         Fp8Tile tile;
-        if (!fp8_find_tile(args, C::BM, C::BN, static_position(t, total, gridDim.x), tile))
+        if (!fp8_find_tile(args, C::BM, C::BN, static_position(t, total, args.round), tile))
             break;
         Loop loop;
         loop.setup(args, tile, tid);
