@@ -188,39 +188,25 @@ __device__ __forceinline__ int fp8_a_row(const Fp8Args &args, int p)
     return min(max(args.rows[p], 0), args.a_rows - 1);
 }
 
-// N consecutive values of one row of D, of which the first `valid` exist.
-template <bool BF16, int N>
-__device__ __forceinline__ void fp8_store_row(void *d, int64_t at, const float (&v)[N], int valid, bool vec)
+// Four consecutive values of one row of D, of which the first `valid` exist.
+template <bool BF16>
+__device__ __forceinline__ void fp8_store4(void *d, int64_t at, const float (&v)[4], int valid, bool vec)
 {
-    constexpr int W = BF16 ? 8 : 4; // elements per 16 bytes
-#pragma unroll
-    for (int c = 0; c < N; c += W) {
-        if (vec && c + W <= valid) {
-            u32x4 w;
-            if constexpr (BF16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf16x2 h = {(__bf16)v[c + 2 * i], (__bf16)v[c + 2 * i + 1]};
-                    w[i] = __builtin_bit_cast(uint32_t, h);
-                }
-                __builtin_nontemporal_store(w, (u32x4 *)((uint16_t *)d + at + c));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = __float_as_uint(v[c + i]);
-                __builtin_nontemporal_store(w, (u32x4 *)((float *)d + at + c));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (c + i < valid) {
-                    if constexpr (BF16)
-                        ((__bf16 *)d)[at + c + i] = (__bf16)v[c + i];
-                    else
-                        ((float *)d)[at + c + i] = v[c + i];
-                }
-        }
+    if (vec && valid >= 4) {
+        if constexpr (BF16)
+            *(bf16x4 *)((__bf16 *)d + at) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        else
+            *(f32x4 *)((float *)d + at) = f32x4{v[0], v[1], v[2], v[3]};
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < valid) {
+            if constexpr (BF16)
+                ((__bf16 *)d)[at + i] = (__bf16)v[i];
+            else
+                ((float *)d)[at + i] = v[i];
+        }
 }
 
 // ---- tiles through LDS -------------------------------------------------------
@@ -237,6 +223,8 @@ struct Fp8Config {
     static constexpr int S_BYTES = THREADS * 4; // one scale per thread, past BM + BN a copy
     static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
     static constexpr int LOADS_A = A_BYTES / 16 / THREADS, LOADS_B = B_BYTES / 16 / THREADS;
+    static constexpr int D_ROW = WTN * (BF16 ? 2 : 4), D_BYTES = WTM * D_ROW; // a wave's piece of D
+    static_assert(WAVES * D_BYTES <= STAGES * STAGE, "the ring holds the tile of D");
     static_assert(BM + BN <= THREADS && BM % 64 == 0 && BN % 64 == 0, "one scale per thread and stage");
     static_assert(NI == 4 && 128 % WTN == 0, "a wave's columns share a block scale, 16 per lane");
     static_assert(STAGES >= 2 && STAGES * STAGE <= 160 * 1024 && (STAGES - 2) * (LOADS_A + LOADS_B + 1) <= 63, "ring");
@@ -477,6 +465,72 @@ template <class C> struct Fp8Wave {
         for (int u = 0; u < STEP; ++u)
             asm volatile("" : "+v"(acc[I][J + u]));
     }
+    // Write the wave's piece of D, through its part `out` of LDS, so that an
+    // instruction writes whole rows of the piece (128 or 256 bytes): straight
+    // from the registers, where a lane holds 16 columns, every instruction
+    // touched each line for a part of it (8192 x 8192 from k = 512: fp32 490 us,
+    // bf16 124). A row's 16-byte chunks are exchanged by the row's number, which
+    // spreads them over the banks.
+    __device__ __forceinline__ void store(const Fp8Args &args, const Fp8Tile &tile, uint8_t *out, int row0, int col0, int lane)
+    {
+        constexpr int ES = C::BF16 ? 2 : 4, CHUNKS = C::D_ROW / 16, W = 16 / ES, ROWS_AT_ONCE = 64 / CHUNKS;
+        const int vm = min(C::WTM, tile.vm - row0), vn = min(C::WTN, tile.vn - col0);
+        if (vm <= 0 || vn <= 0)
+            return;
+        auto place = [](int r, int c) { return r * C::D_ROW + ((c ^ ((C::BF16 ? r >> 1 : r) & (CHUNKS - 1))) << 4); };
+        const int l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int r = i * 16 + l16;
+            if constexpr (C::BF16) {
+#pragma unroll
+                for (int j = 0; j < NI; j += 2) {
+                    u32x4 v;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const f32x4 &s = acc[i][j + h / 2];
+                        const bf16x2 p = {(__bf16)s[2 * (h & 1)], (__bf16)s[2 * (h & 1) + 1]};
+                        v[h] = __builtin_bit_cast(uint32_t, p);
+                    }
+                    *(u32x4 *)(out + place(r, g * 2 + j / 2)) = v;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+                    *(f32x4 *)(out + place(r, g * 4 + j)) = acc[i][j];
+            }
+        }
+        wave_lds_exchange();
+        uint8_t *const d = (uint8_t *)args.d + ((int64_t)(tile.row0 + row0) * args.ldd + tile.col0 + col0) * ES;
+        const int64_t pitch = args.ldd * ES;
+        if (args.d_vec) {
+            const int c = lane % CHUNKS;
+#pragma unroll 4
+            for (int r = lane / CHUNKS; r < C::WTM; r += ROWS_AT_ONCE) {
+                const u32x4 v = *(const u32x4 *)(out + place(r, c));
+                uint8_t *const p = d + r * pitch + c * 16;
+                if (r < vm && (c + 1) * W <= vn)
+                    __builtin_nontemporal_store(v, (u32x4 *)p);
+                else if (r < vm)
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        if (c * W + i < vn) {
+                            if constexpr (C::BF16)
+                                ((uint16_t *)p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+                            else
+                                ((uint32_t *)p)[i] = v[i];
+                        }
+            }
+        } else if (lane < vn) { // rows that start anywhere: one element per lane
+            for (int r = 0; r < vm; ++r) {
+                const uint8_t *const q = out + place(r, lane / W) + lane % W * ES;
+                if constexpr (C::BF16)
+                    *(uint16_t *)(d + r * pitch + lane * 2) = *(const uint16_t *)q;
+                else
+                    *(uint32_t *)(d + r * pitch + lane * 4) = *(const uint32_t *)q;
+            }
+        }
+    }
 };
 
 template <class C>
@@ -624,21 +678,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
             }
             k_block(args.nk - 1, IntC<LAST>{});
         }
-        const int col0 = wn * C::WTN + (lane >> 4) * 16;
-#pragma unroll
-        for (int i = 0; i < C::MI; ++i) {
-            const int row = wm * C::WTM + i * 16 + (lane & 15);
-            if (row < tile.vm && col0 < tile.vn) {
-                float v[16];
-#pragma unroll
-                for (int j = 0; j < C::NI; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[j * 4 + r] = w.acc[i][j][r];
-                fp8_store_row<C::BF16, 16>(args.d, (int64_t)(tile.row0 + row) * args.ldd + tile.col0 + col0, v,
-                                           tile.vn - col0, args.d_vec);
-            }
-        }
+        barrier_lds(); // every wave has read the last stage: the ring takes the results
+        w.store(args, tile, smem + wave * C::D_BYTES, wm * C::WTM, wn * C::WTN, lane);
     }
 }
 
@@ -755,20 +796,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_rows_kernel(const Fp8Args args)
             }
             const int valid = tile.vn - t * 16 - c;
             if (r < tile.vm) {
-                const int64_t at = (int64_t)(tile.row0 + r) * args.ldd + col0 + c;
-                if constexpr (BF16) {
-                    if (args.d_vec && valid >= 4) {
-                        const bf16x4 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-                        *(bf16x4 *)((__bf16 *)args.d + at) = h;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i < valid)
-                                ((__bf16 *)args.d)[at + i] = (__bf16)v[i];
-                    }
-                } else {
-                    fp8_store_row<false, 4>(args.d, at, v, valid, args.d_vec);
-                }
+                fp8_store4<BF16>(args.d, (int64_t)(tile.row0 + r) * args.ldd + col0 + c, v, valid, args.d_vec);
             }
         }
     }
