@@ -82,16 +82,17 @@ gemm_status pts_gemm_fp8(const void *a, int64_t lda, const float *a_scale, int64
  * The same product for each expert over its own rows: rows
  * [offsets[e], offsets[e + 1]) of D are (rows of A) . B_e.
  *
- * offsets: experts + 1 device int32, non-decreasing within [0, m]. Values
- *   outside are taken as the nearest that is not; they cannot lead outside the
- *   operands. Rows of D in no expert's range (before the first offset, behind
- *   the last) are left as they were.
+ * offsets: experts + 1 device int32, non-decreasing within [0, m]; rows of D in
+ *   no expert's range (before the first offset, behind the last) are left as
+ *   they were. Values outside [0, m] are taken as the nearest inside, and a
+ *   table that decreases leaves D's first m rows undefined; neither leads
+ *   outside the operands.
  * rows: device int32 [m], the row of A that each row of D reads (outside
  *   [0, a_rows): the nearest); NULL: row i of D reads row i of A (a_rows >= m).
  * b: expert e at b + e * b_stride_expert, each n x k as in pts_gemm_fp8, with
  *   128 x 128 blocks; b_stride_expert a multiple of 16 elements.
- * 1 <= experts <= PTS_MOE_MAX_EXPERTS. With `rows`, A and its scales must each
- *   span less than 4 GiB (GEMM_ERR_UNSUPPORTED otherwise).
+ * 1 <= experts <= PTS_MOE_MAX_EXPERTS. With `rows`, A must span less than 4 GiB
+ *   and its scales 2 GiB (GEMM_ERR_UNSUPPORTED otherwise).
  */
 gemm_status pts_gemm_fp8_experts(const void *a, int64_t a_rows, int64_t lda, const float *a_scale,
                                  int64_t a_scale_stride_m, int64_t a_scale_stride_k, const void *b, int64_t ldb,

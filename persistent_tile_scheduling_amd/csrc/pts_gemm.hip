@@ -8,7 +8,6 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #define PTS_MAX_GROUPS GEMM_MAX_GROUPS
@@ -19,17 +18,17 @@
 #include "host_error.h"
 
 namespace {
-thread_local std::string g_last_error;
+thread_local char g_last_error[512]; // not a std::string: nothing here may throw into a C caller
 }
 
 gemm_status pts::fail(gemm_status s, const char *fmt, ...)
 {
-    char buf[512];
+    char buf[sizeof g_last_error]; // an argument may be the message kept so far
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
+    memcpy(g_last_error, buf, sizeof buf);
     return s;
 }
 
@@ -501,7 +500,7 @@ const char *gemm_status_string(gemm_status s)
     return "unknown status";
 }
 
-const char *gemm_last_error(void) { return g_last_error.c_str(); }
+const char *gemm_last_error(void) { return g_last_error; }
 
 gemm_status gemm_plan_create(const gemm_desc *desc, gemm_plan **out_plan)
 {

@@ -107,9 +107,9 @@ __device__ __forceinline__ void fp8_raster(int local, int tiles_m, int tiles_n, 
 }
 
 // The tile at position t: the expert is found by a scan of the experts' tile
-// counts, 64 at a time, one per lane. Offsets are clamped into [0, m] and to be
-// non-decreasing, so a bad table cannot lead outside the operands. Returns
-// false past the last tile.
+// counts, 64 at a time, one per lane. Offsets are clamped into [0, m] and an
+// expert's end to its start, so a bad table cannot lead outside the operands.
+// Returns false past the last tile.
 __device__ __forceinline__ bool fp8_find_tile(const Fp8Args &args, int bm, int bn, int t, Fp8Tile &tile)
 {
     if (args.offsets == nullptr) {
@@ -154,7 +154,8 @@ __device__ __forceinline__ bool fp8_find_tile(const Fp8Args &args, int bm, int b
             tile.vm = min(bm, ehi - tile.row0);
             tile.col0 = tn * bn;
             tile.vn = min(bn, args.n - tile.col0);
-            return true;
+            // a table whose ranges overlap can have more tiles than an int counts: nothing beyond this expert's rows
+            return tile.row0 >= elo && tile.vm > 0 && tile.col0 >= 0 && tile.vn > 0;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
     }
@@ -471,8 +472,9 @@ template <class C> struct Fp8Wave {
     // touched each line for a part of it (8192 x 8192 from k = 512: fp32 490 us,
     // bf16 124). A row's 16-byte chunks are exchanged by the row's number, which
     // spreads them over the banks.
-    __device__ __forceinline__ void store(const Fp8Args &args, const Fp8Tile &tile, uint8_t *out, int row0, int col0, int lane)
+    __device__ __forceinline__ void store(const Fp8Args &args, const Fp8Tile &tile, uint8_t *out, int row0, int col0)
     {
+        const int lane = (int)lane_id(); // computed here, so that nothing built on it is kept through the k loop
         constexpr int ES = C::BF16 ? 2 : 4, CHUNKS = C::D_ROW / 16, W = 16 / ES, ROWS_AT_ONCE = 64 / CHUNKS;
         const int vm = min(C::WTM, tile.vm - row0), vn = min(C::WTN, tile.vn - col0);
         if (vm <= 0 || vn <= 0)
@@ -679,7 +681,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
             k_block(args.nk - 1, IntC<LAST>{});
         }
         barrier_lds(); // every wave has read the last stage: the ring takes the results
-        w.store(args, tile, smem + wave * C::D_BYTES, wm * C::WTM, wn * C::WTN, lane);
+        w.store(args, tile, smem + wave * C::D_BYTES, wm * C::WTM, wn * C::WTN);
     }
 }
 

@@ -191,9 +191,11 @@ gemm_status check_product(const void *a, int64_t a_rows, int64_t lda, const floa
     // offsets inside a tile, and from the first to the last k block's scales, are 32-bit byte offsets
     const int64_t limit = (int64_t)1 << 32, nk = ceil_div(k, PTS_FP8_BLOCK);
     const int64_t a_span = gathered ? a_rows : 256;
-    if (lda >= limit / 512 || ldb >= limit / 512 || (gathered && a_span * lda + 128 > limit) || s.a_m >= limit / 4 ||
-        s.b_n >= limit / 4 || s.a_k >= limit / 4 || s.b_k >= limit / 4 || a_span * s.a_m * 4 + nk * s.a_k * 4 > limit ||
-        n * s.b_n * 4 / b_block_n + nk * s.b_k * 4 > limit)
+    auto spans = [&](int64_t rows, int64_t stride_row, int64_t stride_k) { // a scale's; each factor is below 2^31
+        return stride_row >= limit / 4 || stride_k >= limit / 4 || rows * stride_row >= limit / 8 || nk * stride_k >= limit / 8;
+    };
+    if (lda >= limit / 512 || ldb >= limit / 512 || (gathered && a_span * lda + 128 > limit) || spans(a_span, s.a_m, s.a_k) ||
+        spans(ceil_div(n, b_block_n), s.b_n, s.b_k))
         return fail(GEMM_ERR_UNSUPPORTED, "operand or scale strides too large for 32-bit tile offsets");
     if (m == 0 || n == 0)
         return GEMM_OK;

@@ -69,6 +69,8 @@ PRODUCT = dict(a=P, lda=128, sa=P, sam=1, sak=4, b=P, ldb=128, sb=P, sbn=1, sbk=
     (dict(k=2 ** 31, lda=2 ** 31, ldb=2 ** 31), 1, "[0, 2^31)"), (dict(lda=112), 1, "leading"), (dict(ldd=7), 1, "leading"),
     (dict(lda=136), 1, "multiples of 16"), (dict(ldb=136), 1, "multiples of 16"), (dict(sam=-1), 1, "strides"),
     (dict(lda=2 ** 23), 2, "32-bit"), (dict(sak=2 ** 30), 2, "32-bit"), (dict(sbn=2 ** 30), 2, "32-bit"),
+    (dict(sam=2 ** 62), 2, "32-bit"), (dict(sbk=2 ** 62), 2, "32-bit"),
+    (dict(n=2 ** 31 - 1, ldd=2 ** 31, sbn=2 ** 30 - 1, block=1), 2, "32-bit"),
     (dict(a=None), 1, "NULL"), (dict(sb=None), 1, "NULL"), (dict(d=None), 1, "NULL"), (dict(a=P + 8), 1, "16-byte"),
     (dict(sa=P + 2), 1, "4-byte"), (dict(d=P + 2), 1, "element aligned"),
 ])

@@ -290,6 +290,68 @@ def test_experts_with_a_bad_table_stay_inside(pts, per):
     assert torch.equal(d, near)
 
 
+def test_many_experts_of_few_rows(pts):
+    """1024 experts (16 scans of 64), most without rows; a row of A named by several."""
+    n, k, e = 40, 144, 1024
+    rng = np.random.default_rng(8)
+    sizes = (rng.random(e) < 0.2) * rng.integers(1, 40, e)
+    sizes[-1] = 3
+    b = torch.full((e, n, 144), 0, dtype=torch.uint8, device=DEV)
+    b.copy_(_operand(e * n, k, 3)[:, :144].contiguous().view(torch.uint8).view(e, n, k))
+    b = b.view(E4M3)
+    m = int(sizes.sum())
+    a, sa = _operand(7, k, 4), _scale(7, 2, 5)
+    sb = _scale(e, 2, 6, False).view(e, 1, 2)
+    offsets = torch.from_numpy(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)).to(DEV)
+    rows = torch.from_numpy(rng.integers(0, 7, m).astype(np.int32)).to(DEV)
+    for dtype in (BF16, F32):
+        d = pts.gemm_fp8_experts(a, sa, b, sb, offsets, rows, dtype)
+        at = offsets.tolist()
+        for x in np.flatnonzero(sizes):
+            pick = rows[at[x]:at[x + 1]].long()
+            _check_product(d[at[x]:at[x + 1]], a.contiguous().view(torch.uint8)[pick].view(E4M3), sa[pick], b[x], sb[x],
+                           f"expert {x}")
+
+
+# ---- sizes past 32 bits ----------------------------------------------------------
+
+def test_operands_past_four_gigabytes(pts):
+    """The last rows (or the last expert) of operands and results of more than 2^32 bytes equal the same rows on their own."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    k, m = 4096, (1 << 20) + (1 << 17) + 5
+    part = torch.randn((8192, k), device=DEV).to(BF16)
+    x = part.repeat(m // 8192 + 1, 1)[:m]               # 9.7 GB
+    U.log(f"quantise {m} x {k}")
+    q, s = pts.quantize_fp8(x)
+    qp, sp = pts.quantize_fp8(x[m - 100:])
+    assert torch.equal(q[m - 100:].view(torch.uint8), qp.view(torch.uint8)) and torch.equal(s[m - 100:], sp)
+    qt, st = pts.quantize_fp8(x.t())                    # codes of 4096 x m, scales along m
+    qs, ss = pts.quantize_fp8(x[m - 5:].t())            # the last, partial block: m % 128 = 5
+    assert torch.equal(qt[:, m - 5:].contiguous().view(torch.uint8), qs.contiguous().view(torch.uint8))
+    assert torch.equal(st[:, -1:], ss)
+    U.log("product with an A of 4.8 GB, and an output of 4.8 GB")
+    w, ws = pts.quantize_fp8(torch.randn((2048, k), device=DEV), (128, 128))
+    d = pts.gemm_fp8(q, s, w, ws, BF16)
+    assert torch.equal(d[m - 300:], pts.gemm_fp8(q, s, w, ws, BF16)[m - 300:])
+    small = pts.gemm_fp8(qp, sp, w, ws, F32)            # the same rows on their own, fp32
+    # both are within product_bound of the exact value; bf16's rounding is the larger part
+    assert torch.all((d[m - 100:].float() - small).abs() <= small.abs() * 2.0 ** -7 + small.abs().max() * 2.0 ** -9)
+    out = pts.moe_combine(d, torch.ones((4, 2), device=DEV),
+                          torch.tensor([[m - 1, -1], [m - 7, -1], [0, -1], [m - 300, 5]], dtype=torch.int32, device=DEV))
+    assert torch.equal(out[:3], d[[m - 1, m - 7, 0]])
+    del x, qt, d, out
+    U.log("experts whose weights span 5 GB")
+    e, n = 80, 8192
+    b = w.repeat(4, 2).view(torch.uint8).repeat(e, 1).view(e, n, 2 * k).view(E4M3)
+    sb = ws.repeat(4, 2).repeat(e, 1).view(e, n // 128, 2 * k // 128)
+    a, sa = pts.quantize_fp8(torch.randn((e, 2 * k), device=DEV))
+    offsets = torch.arange(e + 1, dtype=torch.int32, device=DEV)
+    d = pts.gemm_fp8_experts(a, sa, b, sb, offsets)
+    for x in (0, e - 1):
+        assert torch.equal(d[x:x + 1], pts.gemm_fp8(a[x:x + 1], sa[x:x + 1], b[x], sb[x], BF16)), x
+
+
 # ---- routing -------------------------------------------------------------------
 
 def _logits(m, e, dtype, seed, closed=0.0, ties=False):
@@ -328,7 +390,7 @@ def test_route(pts, m, experts, k, groups, keep, score, bias, pair, renorm, dtyp
     assert np.array_equal(r.positions.cpu().numpy(), positions)
     # x - max is rounded once (its size in steps), exp is good to 2 steps, up to 1024 terms are added in chains of at
     # most 16 per lane and 6 across, a few products and divisions: span + 32 steps, twice (numerator and denominator)
-    span = float(np.abs(x[torch.isfinite(x)].float()).max()) * 2 if torch.isfinite(x).any() else 0.0
+    span = float(x[torch.isfinite(x)].float().abs().max()) * 2 if torch.isfinite(x).any() else 0.0
     assert np.all(np.abs(_f64(r.weights) - w) <= np.abs(w) * 2 * (span + 32) * 2.0 ** -24)
 
 
@@ -553,6 +615,29 @@ def test_every_operator_replays_from_a_graph(pts):
         torch.cuda.synchronize()
         for j, (p, q) in enumerate(zip(got, step())):
             assert torch.equal(p, q), (i, j)
+
+
+def test_two_graphs_of_the_router_share_nothing(pts):
+    """Two captured routings (with workspaces) replayed at once on two streams."""
+    xs = [torch.randn((3000 + 500 * i, 64), device=DEV) for i in range(2)]
+    pts.moe_route(xs[0], 4)
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(pts.moe_route(x, 4))
+        graphs.append(g)
+    want = [pts.moe_route(x, 4) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(p, q))
 
 
 def test_calls_on_several_streams_at_once(pts):
