@@ -139,38 +139,27 @@ __device__ __forceinline__ void scan_totals(const RouteArgs &args, const int32_t
     __syncthreads();
 }
 
-// Place the slots [first, first + count): `at[e]` is the position of the first
-// of them with expert e. The waves take consecutive parts, 64 slots at a time:
-// a slot's rank among those is the number of lower lanes with the same expert,
-// found by one ballot per bit of the expert's index.
-__device__ __forceinline__ void place_slots(const RouteArgs &args, int64_t first, int count, const int32_t *at,
+constexpr int ORDER_KEPT = 4; // slots per lane whose experts stay in registers (a chunk of 2048)
+
+// The experts of slots lo, lo + 64, .. of this lane, below hi (E + 1: no slot).
+__device__ __forceinline__ void keep_experts(const RouteArgs &args, int64_t first, int lo, int hi, int (&kept)[ORDER_KEPT])
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < ORDER_KEPT; ++i)
+        kept[i] = lo + i * 64 + lane < hi ? slot_expert(args, first + lo + i * 64 + lane) : args.experts + 1;
+}
+
+// Place the slots [first + lo, first + hi) of this wave, 64 at a time: a slot's
+// rank among those is the number of lower lanes with the same expert, found by
+// one ballot per bit of the expert's index. cursor[e]: the next position.
+__device__ __forceinline__ void place_slots(const RouteArgs &args, int64_t first, int lo, int hi, const int (&kept)[ORDER_KEPT],
                                             int32_t *cursor)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = args.experts + 1;
-    for (int i = threadIdx.x; i < ORDER_WAVES * n; i += ORDER_THREADS)
-        cursor[i] = 0;
-    __syncthreads();
-    const int part = (count + ORDER_THREADS - 1) / ORDER_THREADS * 64;
-    const int lo = min(count, wave * part), hi = min(count, lo + part);
-    int32_t *const mine = cursor + wave * n;
-    for (int i = lo + lane; i < hi; i += 64)
-        atomicAdd(&mine[slot_expert(args, first + i)], 1);
-    __syncthreads();
-    for (int e = threadIdx.x; e < n; e += ORDER_THREADS) {
-        int p = at[e];
-#pragma unroll
-        for (int w = 0; w < ORDER_WAVES; ++w) {
-            const int c = cursor[w * n + e];
-            cursor[w * n + e] = p;
-            p += c;
-        }
-    }
-    __syncthreads();
-    const int bits = 32 - __builtin_clz(args.experts);
-    for (int i0 = lo; i0 < hi; i0 += 64) {
-        const bool on = i0 + lane < hi;
-        const int e = on ? slot_expert(args, first + i0 + lane) : 0;
-        uint64_t same = __ballot(on);
+    const int lane = threadIdx.x & 63, bits = 32 - __builtin_clz(args.experts + 1);
+    auto place64 = [&](int i0, int e) {
+        const bool on = e <= args.experts;
+        uint64_t same = ~0ull;
         for (int b = 0; b < bits; ++b) {
             const bool bit = e >> b & 1;
             const uint64_t set = __ballot(bit);
@@ -179,15 +168,21 @@ __device__ __forceinline__ void place_slots(const RouteArgs &args, int64_t first
         const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
         int p = 0;
         if (on)
-            p = mine[e] + rank;
+            p = cursor[e] + rank;
         wave_lds_exchange();
         if (on) {
             place_slot(args, (int)(first + i0 + lane), e, p);
             if (rank == 0)
-                mine[e] = p + __builtin_popcountll(same);
+                cursor[e] = p + __builtin_popcountll(same);
         }
         wave_lds_exchange();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < ORDER_KEPT; ++i)
+        if (lo + i * 64 < hi)
+            place64(lo + i * 64, kept[i]);
+    for (int i0 = lo + ORDER_KEPT * 64; i0 < hi; i0 += 64)
+        place64(i0, i0 + lane < hi ? slot_expert(args, first + i0 + lane) : args.experts + 1);
 }
 
 __global__ __launch_bounds__(ORDER_THREADS) void order_count_kernel(const RouteArgs args)
@@ -205,51 +200,69 @@ __global__ __launch_bounds__(ORDER_THREADS) void order_count_kernel(const RouteA
         args.counts[(int64_t)blockIdx.x * (args.experts + 1) + e] = counts[e];
 }
 
-// One chunk per workgroup. With several chunks each adds up all chunks' counts
-// itself (at most 256 x 1025 words, from L2), which saves a launch in between.
+// Up to so many chunks every workgroup of the order counts all slots itself.
+constexpr int ORDER_SELF_COUNTED = 4;
+
+// One chunk per workgroup; its waves take consecutive parts. Each workgroup adds
+// up all chunks' counts (at most 256 x 1025 words, from L2), or with few chunks
+// counts all slots, which saves a launch.
 __global__ __launch_bounds__(ORDER_THREADS) void order_place_kernel(const RouteArgs args)
 {
-    __shared__ int32_t total[ROUTE_MAX_EXPERTS + 1], before[ROUTE_MAX_EXPERTS + 1];
+    __shared__ int32_t total[ROUTE_MAX_EXPERTS + 1], before[ROUTE_MAX_EXPERTS + 1], earlier[ROUTE_MAX_EXPERTS + 1];
     __shared__ int32_t cursor[ORDER_WAVES * (ROUTE_MAX_EXPERTS + 1)];
-    constexpr int PER = ROUTE_MAX_EXPERTS / ORDER_THREADS + 1;
-    const int n = args.experts + 1, chunk = blockIdx.x;
+    const int n = args.experts + 1, chunk = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t first = (int64_t)chunk * args.chunk, slots = (int64_t)args.m * args.top;
     const int count = (int)min((int64_t)args.chunk, slots - first);
-    int32_t mine[PER]; // slots of this thread's experts in earlier chunks
-    if (args.chunks == 1) {
-        for (int e = threadIdx.x; e < n; e += ORDER_THREADS)
-            total[e] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < count; i += ORDER_THREADS)
-            atomicAdd(&total[slot_expert(args, i)], 1);
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * ORDER_THREADS + threadIdx.x;
-        mine[i] = 0;
-        if (args.chunks > 1 && e < n) {
-            int sum = 0;
+    const int part = (count + ORDER_THREADS - 1) / ORDER_THREADS * 64;
+    const int lo = min(count, wave * part), hi = min(count, lo + part);
+    int kept[ORDER_KEPT];
+    keep_experts(args, first, lo, hi, kept);
+    for (int i = threadIdx.x; i < ORDER_WAVES * n; i += ORDER_THREADS)
+        cursor[i] = 0;
+    const bool self = args.chunks <= ORDER_SELF_COUNTED;
+    for (int e = threadIdx.x; e < n; e += ORDER_THREADS) {
+        int sum = 0, mine = 0;
+        if (!self) {
 #pragma unroll 16
             for (int c = 0; c < args.chunks; ++c) {
                 const int v = args.counts[(int64_t)c * n + e];
-                mine[i] += c < chunk ? v : 0;
+                mine += c < chunk ? v : 0;
                 sum += v;
             }
-            total[e] = sum;
+        }
+        total[e] = sum;
+        earlier[e] = mine;
+    }
+    __syncthreads();
+    int32_t *const mine = cursor + wave * n;
+#pragma unroll
+    for (int i = 0; i < ORDER_KEPT; ++i)
+        if (kept[i] < n)
+            atomicAdd(&mine[kept[i]], 1);
+    for (int i = lo + ORDER_KEPT * 64 + lane; i < hi; i += 64)
+        atomicAdd(&mine[slot_expert(args, first + i)], 1);
+    if (self)
+        for (int i = threadIdx.x; i < slots; i += ORDER_THREADS) {
+            const int e = slot_expert(args, i);
+            atomicAdd(&total[e], 1);
+            if (i < first)
+                atomicAdd(&earlier[e], 1);
+        }
+    __syncthreads();
+    scan_totals(args, total, before);
+    for (int e = threadIdx.x; e < n; e += ORDER_THREADS) {
+        if (chunk == 0)
+            args.offsets[e] = before[e];
+        int p = before[e] + earlier[e];
+#pragma unroll
+        for (int w = 0; w < ORDER_WAVES; ++w) {
+            const int c = cursor[w * n + e];
+            cursor[w * n + e] = p;
+            p += c;
         }
     }
     __syncthreads();
-    scan_totals(args, total, before);
-    if (chunk == 0)
-        for (int e = threadIdx.x; e < n; e += ORDER_THREADS)
-            args.offsets[e] = before[e];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (i * ORDER_THREADS + threadIdx.x < n)
-            before[i * ORDER_THREADS + threadIdx.x] += mine[i];
-    __syncthreads();
-    place_slots(args, first, count, before, cursor);
+    place_slots(args, first, lo, hi, kept, mine);
 }
 
 // Few slots, their experts in LDS (E for none), by the 256 threads of the one

@@ -360,7 +360,7 @@ int64_t pts_moe_route_workspace(int64_t m, int32_t experts, int32_t top)
     if (m <= 0 || experts <= 0 || top <= 0)
         return 0;
     order_chunks(m * top, &chunk, &chunks);
-    return chunks <= 1 ? 0 : chunks * (experts + 1) * (int64_t)sizeof(int32_t);
+    return chunks <= pts::ORDER_SELF_COUNTED ? 0 : chunks * (experts + 1) * (int64_t)sizeof(int32_t);
 }
 
 gemm_status pts_moe_route(const void *logits, int32_t dtype, int64_t ld, const float *bias, int64_t m, int32_t experts,
@@ -414,7 +414,7 @@ gemm_status pts_moe_route(const void *logits, int32_t dtype, int64_t ld, const f
         if (st != GEMM_OK || offsets == nullptr || args.fused)
             return st;
     }
-    if (chunks > 1)
+    if (chunks > pts::ORDER_SELF_COUNTED)
         st = launch(&pts::order_count_kernel, dim3((uint32_t)chunks), pts::ORDER_THREADS, args, stream);
     return st != GEMM_OK ? st
                          : launch(&pts::order_place_kernel, dim3((uint32_t)chunks), pts::ORDER_THREADS, args, stream);
