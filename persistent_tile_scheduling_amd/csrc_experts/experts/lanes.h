@@ -19,6 +19,7 @@ template <int D, class F> __device__ __forceinline__ uint32_t reduce_step(uint32
         return f(r[0], r[1]);
     }
 }
+template <int LPT, class F> __device__ __forceinline__ uint32_t reduce_lanes(float v, F f) = delete; // by its bits
 template <int LPT, class F> __device__ __forceinline__ uint32_t reduce_lanes(uint32_t v, F f)
 {
     v = reduce_step<8>(v, f);

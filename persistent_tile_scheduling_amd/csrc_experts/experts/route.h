@@ -501,6 +501,19 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
     const int experts = args.experts;
     const int64_t token = (int64_t)blockIdx.x * TOKENS + slot;
     const bool live = token < args.m;
+    // this lane's slots, j = q 16 + lane % 16, and their logits: asked for first, they are used last
+    int id[ROUTE_MAX_TOP / 16];
+    float dw[ROUTE_MAX_TOP / 16], chosen[ROUTE_MAX_TOP / 16];
+#pragma unroll
+    for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q) {
+        const int j = q * 16 + (lane & 15);
+        id[q] = -1;
+        dw[q] = 0.f;
+        if (live && j < args.top) {
+            id[q] = args.ids[token * args.top + j];
+            dw[q] = args.dweights[token * args.top + j];
+        }
+    }
     float x[VPL], top = -INFINITY;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -508,7 +521,15 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
         x[v] = live && e < experts ? load_logit(args.logits, args.bf16, token * args.ld + e) : -INFINITY;
         top = fmaxf(top, x[v]);
     }
-    top = reduce_lanes<LPT>(top, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+    for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q) {
+        if (id[q] < 0 || id[q] >= experts) {
+            id[q] = -1;
+            dw[q] = 0.f;
+        }
+        chosen[q] = id[q] >= 0 ? load_logit(args.logits, args.bf16, token * args.ld + id[q]) : 0.f;
+    }
+    top = max_lanes<LPT>(top);
     top = top == -INFINITY ? 0.f : top;
     float p[VPL], total = 0.f;
 #pragma unroll
@@ -523,21 +544,12 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
         for (int v = 0; v < VPL; ++v)
             p[v] /= total;
     }
-    // this lane's slots: j = q 16 + lane % 16
-    int id[ROUTE_MAX_TOP / 16];
-    float dw[ROUTE_MAX_TOP / 16], score[ROUTE_MAX_TOP / 16], sum = 0.f, dot = 0.f;
+    float score[ROUTE_MAX_TOP / 16], sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q) {
-        const int j = q * 16 + (lane & 15);
-        id[q] = live && j < args.top ? args.ids[token * args.top + j] : -1;
-        if (id[q] >= experts)
-            id[q] = -1;
-        dw[q] = score[q] = 0.f;
-        if (id[q] >= 0) {
-            dw[q] = args.dweights[token * args.top + j];
-            const float v = load_logit(args.logits, args.bf16, token * args.ld + id[q]);
-            score[q] = args.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / total;
-        }
+        score[q] = 0.f;
+        if (id[q] >= 0)
+            score[q] = args.sigmoid ? 1.f / (1.f + expf(-chosen[q])) : expf(chosen[q] - top) / total;
         sum += score[q];
         dot += dw[q] * score[q];
     }
@@ -554,20 +566,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
         dp[v] = 0.f;
-    for (int j = 0; j < args.top; ++j) {
-        int e = -1;
-        float d = 0.f;
-#pragma unroll
-        for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
-            if (j / 16 == q) {
-                e = __shfl(id[q], (threadIdx.x & 48) + j % 16);
-                d = __shfl(dw[q], (threadIdx.x & 48) + j % 16);
-            }
+    static_for<ROUTE_MAX_TOP>([&](auto slot) { // each slot in turn to every lane of its row
+        constexpr int Q = decltype(slot)::value / 16, TO_ROW = 0x150 + decltype(slot)::value % 16;
+        if (decltype(slot)::value >= args.top)
+            return;
+        const int e = __builtin_amdgcn_mov_dpp(id[Q], TO_ROW, 0xF, 0xF, false);
+        const float d = __uint_as_float(
+            (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(dw[Q]), TO_ROW, 0xF, 0xF, false));
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (v * LPT + lane == e)
-                dp[v] += d;
-    }
+            dp[v] += v * LPT + lane == e ? d : 0.f;
+    });
     if (live) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {

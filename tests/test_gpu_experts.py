@@ -463,6 +463,29 @@ def test_route_backward(pts, m, experts, k, score, renorm, dtype):
             assert abs(want[t, e] - diff) <= 1e-6 * (1 + abs(diff))
 
 
+@pytest.mark.parametrize("shift", [-300.0, 300.0, -3e38, 2e38])
+@pytest.mark.parametrize("m,experts", [(3, 40), (5, 300), (4200, 64)])
+def test_route_far_from_zero(pts, shift, m, experts):
+    """The softmax and its gradient do not depend on where the logits lie."""
+    base = torch.randint(-8, 9, (m, experts), generator=torch.Generator().manual_seed(m)).float()
+    x = base + shift if abs(shift) < 1e6 else torch.where(base > 0, torch.tensor(shift), torch.tensor(shift) * 1.1)
+    if shift == -300.0:
+        x[0] = base[0] - 5000.0
+    r = pts.moe_route(x.to(DEV), 4)
+    ids, w, *_ = R.route(_f64(x), 4)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert np.all(np.abs(_f64(r.weights) - w) <= np.abs(w) * 2 * (20 + 32) * 2.0 ** -24)      # the spans are at most 16
+    dw = torch.randn((m, 4), generator=torch.Generator().manual_seed(1))
+    for renorm in (True, False):
+        dx = pts.moe_route_backward(dw.to(DEV), x.to(DEV), r.ids, renormalize=renorm)
+        want = R.route_backward(_f64(dw), _f64(x), ids, "softmax", renorm, 1.0)
+        size = np.abs(_f64(dw)).sum(1, keepdims=True) * (2 / w.sum(1, keepdims=True) if renorm else 1)
+        p = np.stack([R.scores(row, "softmax") for row in _f64(x)])
+        got = np.take_along_axis(p, ids, 1).sum(1, keepdims=True)
+        bound = 8 * (20 + 32 + 4) * 2.0 ** -24 * size * p / np.minimum(got, 1)
+        assert np.all(np.abs(_f64(dx) - want) <= bound)
+
+
 def test_route_backward_ids_twice_and_outside(pts):
     x = _logits(3, 20, F32, 4)
     ids = torch.tensor([[1, 1, 2], [-1, 25, 7], [-1, -1, 1 << 30]], dtype=torch.int32)
