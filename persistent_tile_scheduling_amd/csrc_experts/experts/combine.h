@@ -7,7 +7,9 @@
 // row: it adds nothing and its dw is 0; a position -2 - p with p a row (a slot
 // the order put behind the last expert) makes row p of dy zero.
 //
-// Memory bound: y is read once in each direction, dy written once.
+// Memory bound: y is read once in each direction, dy written once. 8192 tokens x
+// 8 rows x 4096, bf16: the sum 119 us (5.1 TB/s; a large copy reaches 5.3), the
+// gradients 253 us (4.5 TB/s); 16 tokens: 4.3 us, the latency of one pass.
 #pragma once
 
 #include "device/common.h"
@@ -82,8 +84,8 @@ template <bool BF16> struct Piece { // 16 bytes of a row
     }
 };
 
-// Rows in flight per thread. 8192 tokens x 8 rows x 4096, bf16: sum 99 us with 4
-// (6.1 TB/s), 109 with 8, 100 with 2; gradients 240, 245, 255 (4.8 TB/s).
+// Rows in flight per thread: with 8 the sum takes 10% longer at that size and the
+// gradients 2%, with 2 1% and 6%.
 constexpr int COMBINE_UNROLL = 4;
 
 // One token's strip of 256 pieces per workgroup.

@@ -132,8 +132,9 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(
 // workgroup walks `rows_per_group` rows of one 512-wide strip; the strip's
 // scales are collected in LDS and written together, since they are stored with
 // the rows next to each other (one k block's scales of consecutive rows are
-// what a product's tile reads). 8192 x 7000 with the gate, bf16: 55 us (5.3
-// TB/s, a large copy's rate) with 8 rows per workgroup, 59 with 4 or 32.
+// what a product's tile reads). 8192 x 7000 with the gate, bf16: 60 us (4.8
+// TB/s; a large copy reaches 5.3) with 8 rows per workgroup, 7% more with 4 or 32.
+// One row of 4096: 2.7 us, the latency of one pass.
 template <bool BF16, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs args)
 {
@@ -195,7 +196,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
 // consecutive lines. The codes leave through LDS, so that a row's 128 codes are
 // written as whole 16-byte pieces; there, row r's sixteen 8-byte pieces are
 // exchanged by a number that follows the thread that writes them, which spreads
-// the 16 lanes' rows over the banks. 5000 x 7000 fp32 by columns: 36 us (4.9 TB/s).
+// the 16 lanes' rows over the banks. 5000 x 7000 fp32 by columns: 42 us (4.2
+// TB/s; its columns start inside cache lines, which adds 16% to what is read).
 template <bool BF16, bool COL, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs args)
 {

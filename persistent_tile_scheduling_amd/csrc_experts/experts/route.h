@@ -12,6 +12,10 @@
 // (32 bits, exactly). An expert is open to a token if its logit and its c are
 // above -inf (and not NaN); a slot for which no open expert is left gets id -1
 // and weight 0. A row whose softmax is not a number goes by its logits.
+//
+// Latency and instruction bound: 16384 tokens x 128 experts, 8 each, fp32 (10 MB
+// in all, 2 us of memory time): choice 11 us, counts 4, order 7.4, gradient 8.5.
+// One token of 256 experts with groups: 7.5 us in one launch.
 #pragma once
 
 #include "lanes.h"
@@ -342,7 +346,10 @@ __device__ __forceinline__ uint64_t keep_groups(const RouteArgs &args, double *c
 }
 
 // A token is held by LPT lanes, VPL logits each (expert v LPT + lane). WIDE:
-// the choice goes by 64-bit scores (a bias), otherwise by the logits.
+// the choice goes by 64-bit scores (a bias), otherwise by the logits. 16 lanes
+// per token keep every reduction inside a row of lanes (four rotations, no
+// exchange between rows) and four tokens in a wave; 64 lanes leave the least
+// work per lane where there are few tokens or many experts.
 template <int LPT, int VPL, bool WIDE>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
 {
@@ -422,8 +429,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
                 if (!(kept >> (min(v * LPT + lane, experts - 1) / size) & 1))
                     key[v] = 0;
         }
-        // The best ones in turn: the largest key, of those the largest low half, of those the lowest index. Slot j
-        // belongs to lane j % 16 (of every row of lanes).
+        // The best ones in turn: the largest key, of those the largest low half, of those the lowest
+        // index. Slot j belongs to lane j % 16 (of every row of lanes).
         int id[ROUTE_MAX_TOP / 16];
 #pragma unroll
         for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)

@@ -61,6 +61,7 @@ template <class Args> gemm_status launch_blocks(void (*kernel)(Args), int64_t bl
 }
 
 bool aligned(const void *p, size_t to) { return ((uintptr_t)p % to) == 0; }
+constexpr int64_t MAX_EXTENT = INT32_MAX - 1024; // kernels round an extent up to whole tiles in 32 bits
 bool in_range(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
 // ---- products ------------------------------------------------------------------
@@ -124,14 +125,14 @@ template <class C> gemm_status launch_tiles(pts::Fp8Args &args, int cus, void *s
 // 256 x 256 tiles (bf16 results) once they reach 55% of the compute units:
 // 2048 x 8192 x 8192 128 against 141 with 128 x 128; 2048 x 4096 x 4096 (half of
 // the units) 41 with 128 x 128. Experts need more than 192 rows each (64
-// experts, 4096 x 4096: 224 rows 389 against 425, 160 rows 128 x 128: 334). For
-// fp32 results, whose widened operands keep the vector units busy, 128 x 128 is
-// as good or better throughout (4096 x 8192 x 8192: 603 against 665 with 256 x
-// 128), two independent workgroups per compute unit hiding each other's waits.
+// experts, 4096 x 4096: 224 rows 389 against 425, 160 rows 334 with 128 x 128).
+// For fp32 results, whose widened operands keep the vector units busy, 128 x 128
+// is as good or better throughout (4096 x 8192 x 8192: 603 against 665 with 256 x
+// 128): two independent workgroups per compute unit hide each other's waits.
 //
 // 64 x 128 tiles while 128 x 128 ones would not outnumber the compute units
-// (1024 x 4096 x 4096: 24 against 31; 768 x 8192 x 8192: 64 against 59), and for
-// experts of up to 64 rows.
+// (1024 x 4096 x 4096, 256 tiles: 24 against 31; 768 x 8192 x 8192, 384 tiles: 64
+// against 59), and for experts of up to 64 rows.
 template <bool ROWS, bool BF16> gemm_status run_tiles(pts::Fp8Args &args, int64_t together, int cus, void *stream)
 {
     if constexpr (BF16)
@@ -142,10 +143,12 @@ template <bool ROWS, bool BF16> gemm_status run_tiles(pts::Fp8Args &args, int64_
     return launch_tiles<pts::Fp8Config<64, 128, 2, 2, 3, ROWS, BF16>>(args, cus, stream);
 }
 
-// The kernel without LDS up to 4 rows per expert (2 rows each 159 against 167
-// with 64 x 128 tiles, 8 rows 235 against 211), and for one product up to 32
-// rows, or 64 for fp32 results (32 x 4096 x 4096: 9.5 against 14.7; 64 rows bf16:
-// 13.1 and 14.9, 64 x 8192 x 8192: 43 and 26; fp32 14 and 29, 44 and 53).
+// The kernel without LDS up to 4 rows per expert (64 experts, 4096 x 4096, 2 rows
+// each: 159 against 167 with 64 x 128 tiles, 8 rows 235 against 211); for one
+// product up to 32 rows (32 x 4096 x 4096: 9.5 against 14.7), or 64 for fp32
+// results (64 x 4096 x 4096: 14 against 29; 64 x 8192 x 8192: 44 against 53). With
+// 64 rows and bf16 results the tiles lose 1.8 us of 14.9 at the first of these
+// sizes and gain 17 of 43 at the second.
 gemm_status run_product(pts::Fp8Args &args, bool rows, bool bf16, void *stream)
 {
     int cus = 0;
@@ -197,6 +200,8 @@ gemm_status check_product(const void *a, int64_t a_rows, int64_t lda, const floa
     if (lda >= limit / 512 || ldb >= limit / 512 || (gathered && a_span * lda + 128 > limit) || spans(a_span, s.a_m, s.a_k) ||
         spans(ceil_div(n, b_block_n), s.b_n, s.b_k))
         return fail(GEMM_ERR_UNSUPPORTED, "operand or scale strides too large for 32-bit tile offsets");
+    if (std::max(m, n) > MAX_EXTENT)
+        return fail(GEMM_ERR_UNSUPPORTED, "m and n must be below 2^31 - 1024");
     if (m == 0 || n == 0)
         return GEMM_OK;
     if (d == nullptr || (k > 0 && (a == nullptr || b == nullptr || a_scale == nullptr || b_scale == nullptr)))
@@ -261,7 +266,7 @@ gemm_status pts_quantize_fp8(const void *x, int32_t dtype_x, int32_t layout_x, i
     const bool col = layout_x == GEMM_COL_MAJOR;
     if (swiglu && (col || block_m != 1))
         return fail(GEMM_ERR_UNSUPPORTED, "the gated form takes a row-major x and 1 x 128 blocks");
-    if (!in_range(m) || !in_range(k) || k > INT32_MAX - 1024 || m > INT32_MAX - 1024)
+    if (m < 0 || k < 0 || m > MAX_EXTENT || k > MAX_EXTENT)
         return fail(GEMM_ERR_INVALID_VALUE, "m and k must be in [0, 2^31 - 1024)");
     if (ldx < (col ? m : swiglu ? 2 * k : k) || ldq < k)
         return fail(GEMM_ERR_INVALID_VALUE, "leading dimension smaller than the packed extent");
@@ -357,8 +362,8 @@ gemm_status pts_gemm_fp8_experts(const void *a, int64_t a_rows, int64_t lda, con
 int64_t pts_moe_route_workspace(int64_t m, int32_t experts, int32_t top)
 {
     int64_t chunk, chunks;
-    if (m <= 0 || experts <= 0 || top <= 0)
-        return 0;
+    if (m <= 0 || experts <= 0 || top <= 0 || m > INT32_MAX / top)
+        return 0; // nothing to order, or a call that is refused
     order_chunks(m * top, &chunk, &chunks);
     return chunks <= pts::ORDER_SELF_COUNTED ? 0 : chunks * (experts + 1) * (int64_t)sizeof(int32_t);
 }
@@ -381,7 +386,7 @@ gemm_status pts_moe_route(const void *logits, int32_t dtype, int64_t ld, const f
     if (topk_groups * (experts / groups) < top)
         return fail(GEMM_ERR_INVALID_VALUE, "%d groups of %d experts hold fewer than top = %d", topk_groups,
                     experts / groups, top);
-    if (m < 0 || m * top > INT32_MAX)
+    if (m < 0 || m > INT32_MAX / top)
         return fail(GEMM_ERR_INVALID_VALUE, "m * top must be in [0, 2^31)");
     if (ld < experts)
         return fail(GEMM_ERR_INVALID_VALUE, "leading dimension smaller than the packed extent");
@@ -431,7 +436,7 @@ gemm_status pts_moe_route_backward(const float *dweights, const void *logits, in
                     PTS_MOE_MAX_EXPERTS, top, experts);
     if (score != PTS_SCORE_SOFTMAX && score != PTS_SCORE_SIGMOID)
         return fail(GEMM_ERR_INVALID_VALUE, "score must be softmax (0) or sigmoid (1)");
-    if (m < 0 || m * top > INT32_MAX)
+    if (m < 0 || m > INT32_MAX / top)
         return fail(GEMM_ERR_INVALID_VALUE, "m * top must be in [0, 2^31)");
     if (ld < experts || ld_d < experts)
         return fail(GEMM_ERR_INVALID_VALUE, "leading dimension smaller than the packed extent");
@@ -468,8 +473,9 @@ static gemm_status check_combine(int32_t dtype, int64_t ldy, int64_t rows, int64
         return fail(GEMM_ERR_UNSUPPORTED, "y must be bf16 or fp32");
     if (top < 1 || top > PTS_MOE_MAX_TOP)
         return fail(GEMM_ERR_UNSUPPORTED, "1 <= top <= %d (got %d)", PTS_MOE_MAX_TOP, top);
-    if (!in_range(m) || !in_range(rows) || n < 0 || n > (1 << 26) || m * top > INT32_MAX || m >= 1 << 24)
-        return fail(GEMM_ERR_INVALID_VALUE, "m must be in [0, 2^24), rows and m * top in [0, 2^31), n in [0, 2^26]");
+    // one workgroup per token and 1024 or 2048 columns: the grid's limits
+    if (m < 0 || m >= 1 << 24 || m * top > INT32_MAX || !in_range(rows) || n < 0 || n > (1 << 26) - 1024)
+        return fail(GEMM_ERR_INVALID_VALUE, "m must be in [0, 2^24), rows and m * top in [0, 2^31), n in [0, 2^26 - 1024]");
     if (ldy < n || ld_out < n)
         return fail(GEMM_ERR_INVALID_VALUE, "leading dimension smaller than the packed extent");
     return GEMM_OK;

@@ -432,6 +432,8 @@ def moe_fp8(x: torch.Tensor, logits: torch.Tensor, k: int, gate_up: torch.Tensor
     keywords of :func:`moe_route`. Eight launches at most and no host
     synchronisation.
     """
+    _matrix("x", x, _VALUES)
+    _expect("logits", logits, _VALUES, (x.shape[0], None))
     r = moe_route(logits, k, **routing)
     h = gemm_fp8_experts(*quantize_fp8(x), gate_up, gate_up_scale, r.offsets, r.rows)
     y = gemm_fp8_experts(*quantize_fp8(h, swiglu=True), down, down_scale, r.offsets)

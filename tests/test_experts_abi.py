@@ -175,6 +175,33 @@ def test_tensor_checks_come_before_the_device(pts):
             call()
 
 
+@pytest.mark.parametrize("extent", [2 ** 31 - 1, 2 ** 31 - 1023])
+def test_extents_that_do_not_round_up_are_refused(pts, extent):
+    for change in (dict(m=extent, n=1, ldd=1), dict(n=extent, ldd=2 ** 31, block=128)):
+        _refused(pts, lambda: pts.pts_gemm_fp8(*{**PRODUCT, **change}.values(), stream=0), 2, "2^31 - 1024")
+    for change in (dict(m=extent), dict(k=extent, ldx=2 ** 31, ldq=2 ** 31)):
+        _refused(pts, lambda: pts.pts_quantize_fp8(*{**QUANTIZE, **change}.values(), stream=0), 1, "m and k")
+
+
+def test_slot_counts_past_64_bits_are_refused(pts):
+    m = 2 ** 62 + 1  # times 4 is 4 again in 64 bits
+    assert pts.pts_moe_route_workspace(m, 8, 4) == 0
+    _refused(pts, lambda: pts.pts_moe_route(*{**ROUTE, "m": m, "top": 4}.values(), stream=0), 1, "m * top")
+    _refused(pts, lambda: pts.pts_moe_route_backward(*{**BACK, "m": m, "top": 4}.values(), stream=0), 1, "m * top")
+    _refused(pts, lambda: pts.pts_moe_combine(*{**COMBINE, "m": m, "top": 4}.values(), stream=0), 1, "m * top")
+
+
+def test_combined_rows_past_the_grid_are_refused(pts):
+    n = 2 ** 26 - 1023
+    _refused(pts, lambda: pts.pts_moe_combine(*{**COMBINE, "n": n, "ldy": n, "ldo": n}.values(), stream=0), 1, "2^26")
+
+
+def test_layer_needs_logits_of_every_token(pts):
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="logits"):
+        pts.moe_fp8(x, torch.zeros((5, 8)), 2, None, None, None, None)
+
+
 def test_reference_rounding_matches_an_exhaustive_search():
     # the tests' own rounding: against the nearest of all codes, on values around every midpoint
     grid = R.E4M3[:127]
