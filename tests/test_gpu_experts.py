@@ -394,6 +394,24 @@ def test_route(pts, m, experts, k, groups, keep, score, bias, pair, renorm, dtyp
     assert np.all(np.abs(_f64(r.weights) - w) <= np.abs(w) * 2 * (span + 32) * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("m,experts,k", [(2049, 3, 1), (65536, 9, 8), (65537, 9, 8), (70001, 200, 8), (300007, 33, 4)])
+def test_order_of_many_slots(pts, m, experts, k):
+    """Chunks of the order on both sides of 2048 slots each, and of the count that needs no launch of its own."""
+    U.log(f"order {m}x{experts} k {k}")
+    x = _logits(m, experts, F32, m, 0.2, True)
+    x[m // 3:m // 3 + 100] = float("-inf")
+    r = pts.moe_route(x.to(DEV), k)
+    ids = r.ids.cpu().numpy().reshape(-1)
+    assert ids.min() == -1 and ids.max() == experts - 1
+    expert = np.where(ids < 0, experts, ids)
+    order = np.argsort(expert, kind="stable")
+    assert np.array_equal(r.offsets.cpu().numpy(), np.searchsorted(expert[order], np.arange(experts + 1)))
+    assert np.array_equal(r.rows.cpu().numpy(), order // k)
+    position = np.empty_like(order)
+    position[order] = np.arange(len(order))
+    assert np.array_equal(r.positions.cpu().numpy().reshape(-1), np.where(ids < 0, -2 - position, position))
+
+
 def test_route_of_no_tokens_and_strided_logits(pts):
     x = _logits(6, 40, F32, 1).to(DEV)
     r = pts.moe_route(x[:0], 2)
