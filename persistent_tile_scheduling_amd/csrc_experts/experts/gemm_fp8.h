@@ -8,12 +8,13 @@
 // ascending order, one accumulator per output, so a result does not depend on
 // timing.
 //
-// On MI355X: 8192^3 to bf16 442 us, 2490 TFLOP/s. The matrix unit is busy 58% of
-// the cycles; beside each of its 32-cycle instructions stand four multiply-adds
-// (the scales), a quarter of the fragments' LDS reads, and the power limit, which
-// holds the clock at 2.0 of 2.4 GHz. 5000 x 7000 x 3000 to fp32, both operands scaled
-// per row: 235 us, 890 TFLOP/s, bound by the vector instructions (two widenings
-// and over two scalings per 16-cycle matrix instruction).
+// On MI355X: 8192^3 to bf16 430 us, 2560 TFLOP/s. The matrix unit is busy about
+// 60% of the cycles; each of its 32-cycle instructions is followed by four
+// multiply-adds (the scales), and the power limit holds the clock at 2.0 of 2.4
+// GHz, so that cycles saved elsewhere come back as a lower clock. 5000 x 7000 x
+// 3000 to fp32, both operands scaled per row: 230 us, 910 TFLOP/s, bound by the
+// vector instructions (two widenings and over two scalings per 16-cycle matrix
+// instruction).
 #pragma once
 
 #include "device/common.h"
