@@ -12,7 +12,7 @@ namespace pts {
 template <int D, class F> __device__ __forceinline__ uint32_t reduce_step(uint32_t v, F f)
 {
     if constexpr (D < 16) {
-        return f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + D, 0xF, 0xF, false));
+        return f(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + D, 0xF, 0xF, true));
     } else {
         const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
                                : __builtin_amdgcn_permlane32_swap(v, v, false, false);

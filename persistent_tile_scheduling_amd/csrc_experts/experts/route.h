@@ -14,8 +14,8 @@
 // and weight 0. A row whose softmax is not a number goes by its logits.
 //
 // Latency and instruction bound: 16384 tokens x 128 experts, 8 each, fp32 (10 MB
-// in all, 2 us of memory time): choice 11 us, counts 4, order 7.4, gradient 8.5.
-// One token of 256 experts with groups: 7.5 us in one launch.
+// in all, 2 us of memory time): choice 10 us, counts 4, order 7.3, gradient 8.3.
+// One token of 256 experts with groups: 7.3 us in one launch.
 #pragma once
 
 #include "lanes.h"
@@ -346,19 +346,19 @@ __device__ __forceinline__ uint64_t keep_groups(const RouteArgs &args, double *c
 }
 
 // A token is held by LPT lanes, VPL logits each (expert v LPT + lane). WIDE:
-// the choice goes by 64-bit scores (a bias), otherwise by the logits. 16 lanes
+// the choice goes by 64-bit scores (a bias), otherwise by the logits. GROUPED:
+// it is limited to the best groups (a kernel of its own: the group arithmetic
+// held 90 registers through the others' choice, 11 us against 10). 16 lanes
 // per token keep every reduction inside a row of lanes (four rotations, no
 // exchange between rows) and four tokens in a wave; 64 lanes leave the least
 // work per lane where there are few tokens or many experts.
-template <int LPT, int VPL, bool WIDE>
+template <int LPT, int VPL, bool WIDE, bool GROUPED>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
 {
     constexpr int TOKENS = 256 / LPT; // per workgroup and pass
-    constexpr int CHOICE_BYTES = TOKENS * LPT * VPL * 8;
-    __shared__ __align__(8) uint8_t lds[CHOICE_BYTES];
+    __shared__ double group_scores[GROUPED ? TOKENS * LPT * VPL : 1];
     __shared__ int32_t fused_experts[ROUTE_FUSED_SLOTS];
     const int lane = threadIdx.x & (LPT - 1), slot = threadIdx.x / LPT;
-    double *const scores = (double *)lds + slot * LPT * VPL;
     const int experts = args.experts;
     for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < args.m; t0 += (int64_t)gridDim.x * TOKENS) {
         const int64_t token = t0 + slot;
@@ -382,8 +382,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
             total = total == 0.f ? 1.f : total;
         }
         double c[VPL];
-        const bool wide = WIDE || (args.groups > 1 && args.pair);
-        if (wide) {
+        if (WIDE || (GROUPED && args.pair)) {
             double all = 1.;
             if (!args.sigmoid) {
                 all = 0.;
@@ -417,7 +416,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
             key[v] = open ? (uint32_t)(k >> 32) : 0u;
             low[v] = (uint32_t)k;
         }
-        if (args.groups > 1) {
+        if constexpr (GROUPED) {
+            double *const scores = group_scores + slot * LPT * VPL;
             const int size = experts / args.groups;
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
@@ -539,12 +539,16 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
     top = max_lanes<LPT>(top);
     top = top == -INFINITY ? 0.f : top;
     float p[VPL], total = 0.f;
+    if (args.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        p[v] = args.sigmoid ? 1.f / (1.f + expf(-x[v])) : expf(x[v] - top);
-        total += p[v];
-    }
-    if (!args.sigmoid) {
+        for (int v = 0; v < VPL; ++v)
+            p[v] = 1.f / (1.f + expf(-x[v]));
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            p[v] = expf(x[v] - top);
+            total += p[v];
+        }
         total = sum_lanes<LPT>(total);
         total = total == 0.f ? 1.f : total;
 #pragma unroll
@@ -577,9 +581,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
         constexpr int Q = decltype(slot)::value / 16, TO_ROW = 0x150 + decltype(slot)::value % 16;
         if (decltype(slot)::value >= args.top)
             return;
-        const int e = __builtin_amdgcn_mov_dpp(id[Q], TO_ROW, 0xF, 0xF, false);
+        const int e = __builtin_amdgcn_mov_dpp(id[Q], TO_ROW, 0xF, 0xF, true);
         const float d = __uint_as_float(
-            (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(dw[Q]), TO_ROW, 0xF, 0xF, false));
+            (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(dw[Q]), TO_ROW, 0xF, 0xF, true));
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
             dp[v] += v * LPT + lane == e ? d : 0.f;

@@ -228,7 +228,7 @@ void order_chunks(int64_t slots, int64_t *chunk, int64_t *chunks)
     *chunks = ceil_div(slots, *chunk);
 }
 
-template <bool WIDE> gemm_status launch_route(pts::RouteArgs &args, int cus, void *stream)
+template <bool WIDE, bool GROUPED> gemm_status launch_route(pts::RouteArgs &args, int cus, void *stream)
 {
     // 16 lanes per token once that gives every SIMD a wave (four tokens each)
     const bool many = args.m >= 16 * (int64_t)cus;
@@ -237,13 +237,13 @@ template <bool WIDE> gemm_status launch_route(pts::RouteArgs &args, int cus, voi
     int tokens = 4;
     if (many && e <= 256) {
         tokens = 16;
-        k = e <= 64    ? &pts::route_kernel<16, 4, WIDE>
-            : e <= 128 ? &pts::route_kernel<16, 8, WIDE>
-                       : &pts::route_kernel<16, 16, WIDE>;
+        k = e <= 64    ? &pts::route_kernel<16, 4, WIDE, GROUPED>
+            : e <= 128 ? &pts::route_kernel<16, 8, WIDE, GROUPED>
+                       : &pts::route_kernel<16, 16, WIDE, GROUPED>;
     } else {
-        k = e <= 256   ? &pts::route_kernel<64, 4, WIDE>
-            : e <= 512 ? &pts::route_kernel<64, 8, WIDE>
-                       : &pts::route_kernel<64, 16, WIDE>;
+        k = e <= 256   ? &pts::route_kernel<64, 4, WIDE, GROUPED>
+            : e <= 512 ? &pts::route_kernel<64, 8, WIDE, GROUPED>
+                       : &pts::route_kernel<64, 16, WIDE, GROUPED>;
     }
     const int64_t blocks = args.fused ? 1 : ceil_div(args.m, tokens);
     return launch_blocks(k, blocks, 256, args, stream);
@@ -415,7 +415,10 @@ gemm_status pts_moe_route(const void *logits, int32_t dtype, int64_t ld, const f
     // few tokens: one workgroup routes them all and orders their slots, one launch for both
     args.fused = offsets != nullptr && m <= 16 && m * top <= pts::ROUTE_FUSED_SLOTS;
     if (m > 0 || args.fused) {
-        st = bias != nullptr ? launch_route<true>(args, cus, stream) : launch_route<false>(args, cus, stream);
+        if (groups > 1)
+            st = bias != nullptr ? launch_route<true, true>(args, cus, stream) : launch_route<false, true>(args, cus, stream);
+        else
+            st = bias != nullptr ? launch_route<true, false>(args, cus, stream) : launch_route<false, false>(args, cus, stream);
         if (st != GEMM_OK || offsets == nullptr || args.fused)
             return st;
     }
