@@ -380,6 +380,9 @@ template <class C> struct Fp8Wave {
     // one before. The scaled sum of a step is added LAG steps later, so that
     // the multiply-adds run under the matrix instructions that follow.
     static constexpr int STEP = C::EXACT ? 2 : 1, STEPS = MI * NI / STEP, LAG = C::EXACT ? 1 : 2, RING = 2 * LAG;
+    // The sums in flight from one k block to the next belong to the last LAG steps: their columns' scales (ROWS) stay
+    // until those are added, the other columns' are loaded with the next block's fragments.
+    static constexpr int EARLY_COL = NI - LAG * STEP;
     f32x4 acc[MI][NI], sums[RING][STEP];
     Fragment<C::EXACT> a[2], b[NI];
     f32x4 col[NI]; // ROWS: the scales of this lane's columns
@@ -621,19 +624,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
                     }
                 });
                 w.template add<N - Wave::LAG>();
+                if constexpr (C::ROWS && N == Wave::LAG - 1)
+                    static_for<C::NI - Wave::EARLY_COL>([&](auto j) { w.load_col(Wave::EARLY_COL + j.value, stage); });
                 if constexpr (I + 1 == C::MI && MORE)
                     static_for<Wave::STEP>([&](auto u) { w.load_b(J + u.value, next); });
                 keep_order();
             });
-            // ROWS: the sums in flight take the old column scales
-            if constexpr (C::ROWS || !MORE)
-                static_for<Wave::LAG>([&](auto n) { w.template add<Wave::STEPS + n.value - Wave::LAG>(); });
             if constexpr (MORE) {
                 w.load_scales(next);
-                if constexpr (C::ROWS) {
-                    w.late = 0.f;
-                    static_for<C::NI>([&](auto j) { w.load_col(j.value, next); });
-                }
+                static_for<Wave::EARLY_COL>([&](auto j) { w.load_col(j.value, next); });
+            } else {
+                static_for<Wave::LAG>([&](auto n) { w.template add<Wave::STEPS + n.value - Wave::LAG>(); });
             }
             here = after(here);
         };
@@ -668,10 +669,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void gemm_fp8_tile_kernel(const Fp8A
                 k_block_idle(kb);
         } else if (args.nk > 0) {
 #pragma unroll
-            for (int j = 0; j < C::NI; ++j) {
+            for (int j = 0; j < C::NI; ++j)
                 w.load_b(j, smem);
+#pragma unroll
+            for (int j = 0; j < Wave::EARLY_COL; ++j)
                 w.load_col(j, smem);
-            }
             w.load_a(0, 0, smem);
             w.load_scales(smem);
             const int whole = args.k / 128;
