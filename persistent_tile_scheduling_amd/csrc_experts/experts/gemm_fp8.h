@@ -36,7 +36,7 @@ struct Fp8Args {
     int64_t b_expert, sb_expert;    // element strides from one expert's B to the next
     int32_t m, n, k, nk;
     int32_t tiles_n, experts, a_rows;
-    int32_t d_vec; // D's rows are 16-byte aligned
+    int32_t d_vec; // D's rows start at whole 16 bytes (1), at whole cache lines (2)
     int32_t strip; // few rows: 16-column tiles per workgroup
     int32_t round; // tiles: the width of the dealing to the dies
 };
@@ -480,7 +480,9 @@ template <class C> struct Fp8Wave {
     // from the registers, where a lane holds 16 columns, every instruction
     // touched each line for a part of it (8192 x 8192 from k = 512: fp32 490 us,
     // bf16 124). A row's 16-byte chunks are exchanged by the row's number, which
-    // spreads them over the banks.
+    // spreads them over the banks. D streams past the caches, but for bf16 rows
+    // that start inside a line: there two waves write each line, and the L2 joins
+    // them (5000 x 7000 x 3000: 131 us against 141; whole lines and fp32 lose 1 to 3%).
     __device__ __forceinline__ void store(const Fp8Args &args, const Fp8Tile &tile, uint8_t *out, int row0, int col0)
     {
         const int lane = (int)lane_id(); // computed here, so that nothing built on it is kept through the k loop
@@ -515,23 +517,33 @@ template <class C> struct Fp8Wave {
         uint8_t *const d = (uint8_t *)args.d + ((int64_t)(tile.row0 + row0) * args.ldd + tile.col0 + col0) * ES;
         const int64_t pitch = args.ldd * ES;
         if (args.d_vec) {
-            const int c = lane % CHUNKS;
+            auto rows = [&](auto stream) {
+                const int c = lane % CHUNKS;
 #pragma unroll 4
-            for (int r = lane / CHUNKS; r < C::WTM; r += ROWS_AT_ONCE) {
-                const u32x4 v = *(const u32x4 *)(out + place(r, c));
-                uint8_t *const p = d + r * pitch + c * 16;
-                if (r < vm && (c + 1) * W <= vn)
-                    __builtin_nontemporal_store(v, (u32x4 *)p);
-                else if (r < vm)
+                for (int r = lane / CHUNKS; r < C::WTM; r += ROWS_AT_ONCE) {
+                    const u32x4 v = *(const u32x4 *)(out + place(r, c));
+                    uint8_t *const p = d + r * pitch + c * 16;
+                    if (r < vm && (c + 1) * W <= vn) {
+                        if constexpr (stream.value)
+                            __builtin_nontemporal_store(v, (u32x4 *)p);
+                        else
+                            *(u32x4 *)p = v;
+                    } else if (r < vm) {
 #pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        if (c * W + i < vn) {
-                            if constexpr (C::BF16)
-                                ((uint16_t *)p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
-                            else
-                                ((uint32_t *)p)[i] = v[i];
-                        }
-            }
+                        for (int i = 0; i < W; ++i)
+                            if (c * W + i < vn) {
+                                if constexpr (C::BF16)
+                                    ((uint16_t *)p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+                                else
+                                    ((uint32_t *)p)[i] = v[i];
+                            }
+                    }
+                }
+            };
+            if (!C::BF16 || args.d_vec == 2)
+                rows(IntC<1>{});
+            else
+                rows(IntC<0>{});
         } else if (lane < vn) { // rows that start anywhere: one element per lane
             for (int r = 0; r < vm; ++r) {
                 const uint8_t *const q = out + place(r, lane / W) + lane % W * ES;

@@ -213,9 +213,11 @@ gemm_status check_product(const void *a, int64_t a_rows, int64_t lda, const floa
     return GEMM_OK;
 }
 
+// Rows that start at whole 16 bytes (1), at whole cache lines (2), anywhere (0).
 int32_t vector_rows(const void *d, int64_t ldd, int32_t dtype)
 {
-    return aligned(d, 16) && ldd * (dtype == GEMM_DTYPE_BF16 ? 2 : 4) % 16 == 0;
+    const int64_t pitch = ldd * (dtype == GEMM_DTYPE_BF16 ? 2 : 4);
+    return !aligned(d, 16) || pitch % 16 != 0 ? 0 : !aligned(d, 128) || pitch % 128 != 0 ? 1 : 2;
 }
 
 // ---- routing -------------------------------------------------------------------

@@ -181,6 +181,23 @@ def test_product_large_tiles(pts, m, n, k, rows, dtype):
     _check_product(pts.gemm_fp8(a, sa, b, sb, dtype), a, sa, b, sb, "large")
 
 
+@pytest.mark.parametrize("m,n,k,rows", [(3200, 3400, 700, False), (3330, 3102, 384, True), (3328, 3200, 1024, False),
+                                        (3000, 3405, 130, False)])
+def test_product_of_many_large_tiles(pts, m, n, k, rows):
+    """More than half the compute units' worth of 256 x 256 tiles; D's rows at whole lines, whole 16 bytes and anywhere."""
+    U.log(f"product {m}x{n}x{k} rows {rows} bf16")
+    kb = -(-k // 128)
+    a, b = _operand(m, k, 1 + m), _operand(n, k, 2 + n)
+    sa, sb = _scale(m, kb, 3), _scale(n if rows else -(-n // 128), kb, 4, by_column=rows)
+    d = torch.full((m, n + 8), 7.0, dtype=BF16, device=DEV)
+    out = pts.gemm_fp8(a, sa, b, sb, out=d[:, :n])
+    _check_product(out, a, sa, b, sb, f"{m}x{n}x{k}")
+    assert torch.all(d[:, n:] == 7.0)
+    # a slice of the same: its rows start elsewhere, its values are those
+    wide = torch.empty((m, n + 72), dtype=BF16, device=DEV)
+    assert torch.equal(pts.gemm_fp8(a, sa, b, sb, out=wide[:, 8:8 + n]), out)
+
+
 def test_product_of_nothing(pts):
     a, b = _operand(5, 128, 1), _operand(7, 128, 2)
     s = _scale(5, 1, 1)
@@ -265,6 +282,24 @@ def test_experts(pts, sizes, n, k, gather, dtype):
             pick = rows[at[e]:at[e + 1]].long() if gather else torch.arange(at[e], at[e + 1], device=DEV)
             ae = a.contiguous().view(torch.uint8)[pick].view(E4M3)
             _check_product(out[at[e]:at[e + 1]], ae, sa[pick], b[e], sb[e], f"expert {e}")
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n", [3400, 3200])
+def test_experts_in_large_tiles(pts, n, gather):
+    """256 x 256 tiles: experts of less than a tile, exactly one, several and a part, and none."""
+    sizes, k = [600, 0, 300, 900, 257, 256, 255, 0, 100], 300
+    U.log(f"experts {sizes} n {n} k {k} gather {gather}")
+    a, sa, b, sb, offsets, rows, m = _expert_inputs(sizes, n, k, 31, behind=5, gather=gather, before=2)
+    out = torch.full((m, n), 9.0, dtype=BF16, device=DEV)
+    pts.gemm_fp8_experts(a, sa, b, sb, offsets, rows, out=out)
+    o = offsets.cpu().tolist()
+    for e in range(len(sizes)):
+        if sizes[e]:
+            pick = (rows[o[e]:o[e + 1]] if gather else torch.arange(o[e], o[e + 1], device=DEV)).long()
+            ae = a.view(torch.uint8)[pick].view(E4M3)
+            _check_product(out[o[e]:o[e + 1]], ae, sa[pick], b[e], sb[e], f"expert {e}")
+    assert torch.all(out[:o[0]] == 9.0) and torch.all(out[o[-1]:] == 9.0)
 
 
 @pytest.mark.parametrize("per", [2, 100, 300])
