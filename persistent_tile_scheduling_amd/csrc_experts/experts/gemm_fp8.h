@@ -10,9 +10,9 @@
 //
 // On MI355X: 8192^3 to bf16 430 us, 2560 TFLOP/s. The matrix unit is busy about
 // 60% of the cycles; each of its 32-cycle instructions is followed by four
-// multiply-adds (the scales), and the power limit holds the clock at 2.0 of 2.4
-// GHz, so that cycles saved elsewhere come back as a lower clock. 5000 x 7000 x
-// 3000 to fp32, both operands scaled per row: 230 us, 910 TFLOP/s, bound by the
+// multiply-adds (the scales), and the power limit holds the clock at 1.7 to 2.0 of
+// 2.4 GHz, so that cycles saved elsewhere come back as a lower clock. 5000 x 7000 x
+// 3000 to fp32, both operands scaled per row: 225 us, 930 TFLOP/s, bound by the
 // vector instructions (two widenings and over two scalings per 16-cycle matrix
 // instruction).
 #pragma once

@@ -104,6 +104,20 @@ def test_quantize_gated(pts, m, k, dtype):
     assert np.all(np.abs(R.decode(q) * R.expand(s.cpu().numpy(), m, k) - h) <= step * (1 + 2.0 ** -20) + np.abs(h) * rel * 2)
 
 
+@pytest.mark.parametrize("k", [1000, 1003])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("gated", [False, True])
+def test_quantize_many_rows_equals_few(pts, k, dtype, gated):
+    """Workgroups of eight rows, the last one short, against slices that take four."""
+    m = 4101
+    x = _values(m, 2 * k if gated else k, dtype, k).to(DEV)
+    q, s = pts.quantize_fp8(x, swiglu=gated)
+    for lo, hi in ((0, 70), (2047, 2050), (m - 9, m)):
+        qs, ss = pts.quantize_fp8(x[lo:hi], swiglu=gated)
+        assert torch.equal(q[lo:hi].contiguous().view(torch.uint8), qs.contiguous().view(torch.uint8)), (lo, hi)
+        assert torch.equal(s[lo:hi], ss), (lo, hi)
+
+
 def test_quantize_every_e4m3_value_and_midpoint(pts):
     grid = R.E4M3[:127]
     mid = (grid[1:] + grid[:-1]) / 2
@@ -196,6 +210,33 @@ def test_product_of_many_large_tiles(pts, m, n, k, rows):
     # a slice of the same: its rows start elsewhere, its values are those
     wide = torch.empty((m, n + 72), dtype=BF16, device=DEV)
     assert torch.equal(pts.gemm_fp8(a, sa, b, sb, out=wide[:, 8:8 + n]), out)
+
+
+@pytest.mark.parametrize("m,n,k,rows", [(1, 70000, 300, False), (8, 66001, 128, True), (20, 65560, 200, False),
+                                        (50, 66008, 128, True)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_product_of_few_rows_and_many_columns(pts, m, n, k, rows, dtype):
+    """Columns enough for two 16-column tiles per workgroup, the last one alone or ragged."""
+    U.log(f"product {m}x{n}x{k} rows {rows} {dtype}")
+    kb = -(-k // 128)
+    a, b = _operand(m, k, 1 + m), _operand(n, k, 2)
+    sa, sb = _scale(m, kb, 3), _scale(n if rows else -(-n // 128), kb, 4)
+    _check_product(pts.gemm_fp8(a, sa, b, sb, dtype), a, sa, b, sb, f"{m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("n", [2000, 2003])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_experts_of_few_rows_and_many_columns(pts, n, dtype):
+    sizes = [i % 4 for i in range(64)] + [17, 0, 40]
+    U.log(f"67 experts of few rows, n {n} {dtype}")
+    a, sa, b, sb, offsets, rows, m = _expert_inputs(sizes, n, 384, 5, behind=3, gather=True)
+    out = torch.full((m, n), 9.0, dtype=dtype, device=DEV)
+    pts.gemm_fp8_experts(a, sa, b, sb, offsets, rows, out=out)
+    o = offsets.cpu().tolist()
+    for e in [i for i in range(len(sizes)) if sizes[i]]:
+        pick = rows[o[e]:o[e + 1]].long()
+        _check_product(out[o[e]:o[e + 1]], a.view(torch.uint8)[pick].view(E4M3), sa[pick], b[e], sb[e], f"expert {e}")
+    assert torch.all(out[o[-1]:] == 9.0)
 
 
 def test_product_of_nothing(pts):
