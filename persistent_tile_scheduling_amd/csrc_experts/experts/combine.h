@@ -9,7 +9,7 @@
 //
 // Memory bound: y is read once in each direction, dy written once. 8192 tokens x
 // 8 rows x 4096, bf16: the sum 119 us (5.1 TB/s; a large copy reaches 5.3), the
-// gradients 253 us (4.5 TB/s); 16 tokens: 4.3 us, the latency of one pass.
+// gradients 253 us (4.8 TB/s); 16 tokens: 4.3 us, the latency of one pass.
 #pragma once
 
 #include "device/common.h"
@@ -31,11 +31,15 @@ struct CombineArgs {
 template <bool BF16> struct Piece { // 16 bytes of a row
     static constexpr int N = BF16 ? 8 : 4;
     float v[N];
-    __device__ __forceinline__ void load(const void *p, int64_t at, int valid, bool vec)
+    // ONCE: past the caches, for what is read once.
+    template <bool ONCE = true> __device__ __forceinline__ void load(const void *p, int64_t at, int valid, bool vec)
     {
         if (vec && valid >= N) {
-            const u32x4 w = __builtin_nontemporal_load((const u32x4 *)((const uint8_t *)p + at * (BF16 ? 2 : 4)));
-            set(w);
+            const u32x4 *const from = (const u32x4 *)((const uint8_t *)p + at * (BF16 ? 2 : 4));
+            if constexpr (ONCE)
+                set(__builtin_nontemporal_load(from));
+            else
+                set(*from);
             return;
         }
 #pragma unroll
@@ -165,7 +169,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineArgs
         for (int col = threadIdx.x * P::N; col < args.n; col += 256 * P::N) {
             const int valid = args.n - col;
             P d, y[COMBINE_UNROLL];
-            d.load(args.dout, token * args.ld_dout + col, valid, args.vec);
+            d.template load<false>(args.dout, token * args.ld_dout + col, valid, args.vec);
 #pragma unroll
             for (int u = 0; u < COMBINE_UNROLL; ++u)
                 if (pos[u] >= 0 && !dropped[u])
