@@ -9,7 +9,7 @@
 //
 // Memory bound: y is read once in each direction, dy written once. 8192 tokens x
 // 8 rows x 4096, bf16: the sum 119 us (5.1 TB/s; a large copy reaches 5.3), the
-// gradients 253 us (4.8 TB/s); 16 tokens: 4.3 us, the latency of one pass.
+// gradients 238 us (4.8 TB/s); 16 tokens: 4.3 us, the latency of one pass.
 #pragma once
 
 #include "device/common.h"
@@ -88,8 +88,8 @@ template <bool BF16> struct Piece { // 16 bytes of a row
     }
 };
 
-// Rows in flight per thread: with 8 the sum takes 10% longer at that size and the
-// gradients 2%, with 2 1% and 6%.
+// Rows in flight per thread: with 8 both directions take 6% longer at that size,
+// with 2 the sum 1% and the gradients 6%.
 constexpr int COMBINE_UNROLL = 4;
 
 // One token's strip of 256 pieces per workgroup.

@@ -10,7 +10,8 @@
 // Memory bound: 2 or 4 bytes read (twice that with the gate) and 1 byte
 // written per element; each element is read once and kept in registers between
 // the maximum and the conversion. (Loads are ordinary ones: rows need not start
-// at a cache line, and a streaming load would fetch the shared lines twice.)
+// at a cache line, and a streaming load would fetch the shared lines twice. The
+// codes' stores stream: 2% of either form below.)
 #pragma once
 
 #include "lanes.h"
@@ -132,7 +133,7 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(
 // workgroup walks `rows_per_group` rows of one 512-wide strip; the strip's
 // scales are collected in LDS and written together, since they are stored with
 // the rows next to each other (one k block's scales of consecutive rows are
-// what a product's tile reads). 8192 x 7000 with the gate, bf16: 60 us (4.8
+// what a product's tile reads). 8192 x 7000 with the gate, bf16: 55 us (5.2
 // TB/s; a large copy reaches 5.3) with 8 rows per workgroup, 7% more with 4 or 32.
 // One row of 4096: 2.7 us, the latency of one pass.
 template <bool BF16, bool GATED, bool VEC>
@@ -175,7 +176,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
             if (e < room) { // q's rows are padded to whole 16-byte pieces
                 uint8_t *const q = args.q + row * args.ldq + c + e;
                 if constexpr (BF16)
-                    *(uint2 *)q = make_uint2(codes[0], codes[1]);
+                    __builtin_nontemporal_store((uint64_t)codes[1] << 32 | codes[0], (uint64_t *)q);
                 else
                     *(uint32_t *)q = codes[0];
             }
@@ -196,7 +197,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
 // consecutive lines. The codes leave through LDS, so that a row's 128 codes are
 // written as whole 16-byte pieces; there, row r's sixteen 8-byte pieces are
 // exchanged by a number that follows the thread that writes them, which spreads
-// the 16 lanes' rows over the banks. 5000 x 7000 fp32 by columns: 42 us (4.2
+// the 16 lanes' rows over the banks. 5000 x 7000 fp32 by columns: 41 us (4.3
 // TB/s; its columns start inside cache lines, which adds 16% to what is read).
 template <bool BF16, bool COL, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs args)
@@ -279,8 +280,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs a
     for (int i = 0; i < 4; ++i) {
         const int r = i * 32 + tid / 8, piece = (tid & 7) * 2;
         if (r < vm && piece * 8 < room) // q's rows are padded to whole 16-byte pieces
-            *(u32x4 *)(args.q + (int64_t)(row0 + r) * args.ldq + col0 + piece * 8) =
-                *(const u32x4 *)(codes + place(r, piece));
+            __builtin_nontemporal_store(*(const u32x4 *)(codes + place(r, piece)),
+                                        (u32x4 *)(args.q + (int64_t)(row0 + r) * args.ldq + col0 + piece * 8));
     }
     if constexpr (SQUARE) {
         if (tid == 0)
