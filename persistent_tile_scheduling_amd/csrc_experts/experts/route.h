@@ -538,11 +538,13 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
     }
     top = max_lanes<LPT>(top);
     top = top == -INFINITY ? 0.f : top;
-    float p[VPL], total = 0.f;
+    float p[VPL], total = 0.f; // the score, or for the sigmoid its slope
     if (args.sigmoid) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            p[v] = 1.f / (1.f + expf(-x[v]));
+        for (int v = 0; v < VPL; ++v) { // p (1 - p) = z / (1 + z)^2: 1 - p would be lost in the rounding of a p near 1
+            const float z = expf(-fabsf(x[v])), r = 1.f / (1.f + z);
+            p[v] = z * r * r;
+        }
     } else {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = v * LPT + lane;
-            const float d = args.sigmoid ? dp[v] * p[v] * (1.f - p[v]) : p[v] * (dp[v] - back);
+            const float d = args.sigmoid ? dp[v] * p[v] : p[v] * (dp[v] - back);
             if (e < experts) {
                 if (args.bf16)
                     ((__bf16 *)args.dlogits)[token * args.ld_d + e] = (__bf16)d;

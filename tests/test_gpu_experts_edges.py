@@ -1,0 +1,81 @@
+"""GPU tests of the routed-experts operators where they go wrong most easily: scores near their
+limits.
+
+The references are 64-bit. Tolerances are stated where they are used, in units u = 2^-24, half a
+step of fp32 relative to the value.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tests import experts_reference as R
+from tests import gpu_util as U
+
+pytestmark = pytest.mark.gpu
+DEV = U.DEV
+u = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def pts():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import persistent_tile_scheduling_amd as mod
+    return mod
+
+
+def _f64(t):
+    return t.detach().float().cpu().double().numpy()
+
+
+# ---- the router's gradient ---------------------------------------------------------
+
+def _sigmoid_slope(x):
+    """p (1 - p) without the difference: z / (1 + z)^2 with z = exp(-|x|)."""
+    z = np.exp(-np.abs(x))
+    return z / (1 + z) ** 2
+
+
+def _sigmoid_gradient(dw, x, ids, renorm, scale):
+    """The formula's gradient in 64 bits, and the sum of the magnitudes of its terms (both m x experts)."""
+    p, slope = 1 / (1 + np.exp(-x)), _sigmoid_slope(x)
+    dx, size = np.zeros_like(x), np.zeros_like(x)
+    for t in range(x.shape[0]):
+        ok = ids[t] >= 0
+        at, d = ids[t][ok], dw[t][ok]
+        total = p[t, at].sum() + 1e-20 if renorm else 1.0
+        mean, most = ((d * p[t, at]).sum() / total, (np.abs(d) * p[t, at]).sum() / total) if renorm else (0.0, 0.0)
+        np.add.at(dx[t], at, scale / total * (d - mean) * slope[t, at])
+        np.add.at(size[t], at, scale / total * (np.abs(d) + most) * slope[t, at])
+    return dx, size
+
+
+@pytest.mark.parametrize("m,experts,k", [(5, 40, 4), (3, 300, 6), (2, 700, 3), (4200, 24, 2)])
+@pytest.mark.parametrize("low,high", [(10.0, 30.0), (-30.0, -10.0), (60.0, 85.0), (-1.0, 40.0)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_gradient_of_scores_near_one(pts, m, experts, k, low, high, renorm):
+    """The gradient of a score near one is as exact relative to its size as any other's."""
+    U.log(f"sigmoid gradient {m}x{experts} k {k} logits in [{low}, {high}] renormalised {renorm}")
+    rng = np.random.default_rng(m + int(abs(high)))
+    x = torch.from_numpy(rng.uniform(low, high, (m, experts)).astype(np.float32))
+    dw = torch.from_numpy(rng.standard_normal((m, k)).astype(np.float32))
+    ids = torch.from_numpy(np.stack([rng.permutation(experts)[:k] for _ in range(m)]).astype(np.int32))
+    dx = pts.moe_route_backward(dw.to(DEV), x.to(DEV), ids.to(DEV), score="sigmoid", renormalize=renorm, scale=2.5)
+    want, size = _sigmoid_gradient(_f64(dw), _f64(x), ids.numpy(), renorm, 2.5)
+    # exp is good to 2 u, so a score to 4 u (exp 2, sum 1, division 1); dw p then to 5 + k u summed, the scores' sum to
+    # 5 + k, their quotient to 2 k + 11, less dw 1, times scale / sum k + 7: 3 k + 19 u of the terms' magnitude. The slope
+    # is exp (2), two reciprocals of a sum (4 each) and two products: 12 u. Second orders: 1%
+    assert np.all(np.abs(_f64(dx) - want) <= 1.01 * (3 * k + 19 + 12) * u * size)
+    if renorm and low == 10.0:                         # and against differences of the weights in 64 bits
+        z, h = _f64(x)[:1], 1e-2
+        for e in ids[0].tolist():
+            up, dn = z.copy(), z.copy()
+            up[0, e] += h
+            dn[0, e] -= h
+            diff = (_f64(dw)[0] * (R.weights_of(up, ids[:1].numpy(), "sigmoid", True, 2.5) -
+                                   R.weights_of(dn, ids[:1].numpy(), "sigmoid", True, 2.5))).sum() / (2 * h)
+            # h^2 / 6 of the third derivative (at most the first, the scores being 1 - exp(-x)), and the weights' own
+            # 64-bit rounding over 2 h
+            assert abs(want[0, e] - diff) <= 1e-4 * abs(want[0, e]) + 64 * 2.0 ** -53 * 2.5 * np.abs(_f64(dw)[0]).sum() / h
