@@ -147,7 +147,8 @@ int64_t pts_moe_route_workspace(int64_t m, int32_t experts, int32_t top);
  * and the choice `ids` (m x top; -1 or any value outside [0, experts): no
  * expert). dlogits has the logits' dtype, row stride ld_d; all of m x experts is
  * written. The choice has no gradient, so neither has the bias. An expert named
- * twice gets the sum.
+ * twice gets the sum. With sigmoid scores an expert that is not named gets 0,
+ * whatever its logit (a NaN that closes it, say).
  */
 gemm_status pts_moe_route_backward(const float *dweights, const void *logits, int32_t dtype, int64_t ld,
                                    const int32_t *ids, int64_t m, int32_t experts, int32_t top, int32_t score,

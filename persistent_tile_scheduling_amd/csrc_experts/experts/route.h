@@ -499,7 +499,9 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
 //   otherwise:     dL/dp_j = scale dw_j
 //   softmax:       dL/dx_e = p_e (dL/dp_e - sum_j dL/dp_j p_j)
 //   sigmoid:       dL/dx_e = dL/dp_e p_e (1 - p_e)
-// The scores are computed again. An id outside [0, experts) has no score.
+// The scores are computed again. An id outside [0, experts) has no score. A
+// sigmoid's expert that no id names has no part in the weights: 0, also where
+// its logit is a NaN, which closes it.
 template <int LPT, int VPL>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs args)
 {
@@ -594,7 +596,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = v * LPT + lane;
-            const float d = args.sigmoid ? dp[v] * p[v] : p[v] * (dp[v] - back);
+            const float d = !args.sigmoid ? p[v] * (dp[v] - back) : dp[v] == 0.f ? 0.f : dp[v] * p[v];
             if (e < experts) {
                 if (args.bf16)
                     ((__bf16 *)args.dlogits)[token * args.ld_d + e] = (__bf16)d;

@@ -79,3 +79,19 @@ def test_sigmoid_gradient_of_scores_near_one(pts, m, experts, k, low, high, reno
             # h^2 / 6 of the third derivative (at most the first, the scores being 1 - exp(-x)), and the weights' own
             # 64-bit rounding over 2 h
             assert abs(want[0, e] - diff) <= 1e-4 * abs(want[0, e]) + 64 * 2.0 ** -53 * 2.5 * np.abs(_f64(dw)[0]).sum() / h
+
+
+@pytest.mark.parametrize("m,experts", [(5, 40), (4200, 100)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_gradient_of_experts_that_are_closed(pts, m, experts, renorm):
+    """An expert that a NaN closes to a token has no part in its weights: gradient 0, the others' as without it."""
+    x = torch.randn((m, experts), generator=torch.Generator().manual_seed(m)) * 2
+    x[::2, 3] = float("nan")
+    x[1::2, 5] = -float("inf")
+    dw = torch.randn((m, 3), generator=torch.Generator().manual_seed(1)).to(DEV)
+    r = pts.moe_route(x.to(DEV), 3, score="sigmoid", renormalize=renorm)
+    assert not torch.any(torch.isnan(r.weights))
+    dx = pts.moe_route_backward(dw, x.to(DEV), r.ids, score="sigmoid", renormalize=renorm)
+    same = pts.moe_route_backward(dw, torch.nan_to_num(x, nan=0.0, neginf=-float("inf")).to(DEV), r.ids, score="sigmoid",
+                                  renormalize=renorm)
+    assert torch.equal(dx, same) and torch.all(dx[::2, 3] == 0) and torch.all(dx[1::2, 5] == 0)
