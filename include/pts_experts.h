@@ -45,8 +45,9 @@ typedef enum { PTS_SCORE_SOFTMAX = 0, PTS_SCORE_SIGMOID = 1 } pts_score;
  * block_m: 1 or 128 rows per block (always 128 k).
  * swiglu: non-zero quantises g / (1 + exp(-g)) * u instead, where row i of x
  *   holds g in its first k and u in its next k elements (so 2 k per row);
- *   row-major, block_m = 1 only. The product is formed in fp32 and not rounded
- *   in between.
+ *   row-major, block_m = 1 only. The product is formed in fp32, to 7 * 2^-24 of
+ *   its value (for g below -87 also to 2^-149 |g u|, exp's least step), and not
+ *   rounded in between.
  * q: m rows of k codes, row stride ldq >= k, a multiple of 16, q 16-byte
  *   aligned; the bytes from k up to the next multiple of 16 are written as 0.
  * scale: element (row or row block i, k block b) at i * scale_stride_m +

@@ -67,6 +67,26 @@ template <int N> __device__ __forceinline__ void quantize(const float *x, float 
         out[i / 4] = pack4(t[i], t[i + 1], t[i + 2], t[i + 3]);
 }
 
+// silu(g) = g / (1 + exp(-g)) in fp32. Up to |g| = 87, to 6 2^-24 of its value
+// (the compiler's expf and division, to 5, made the gated form of 8192 x 7000
+// 77 us instead of 62):
+//   t = g / ln 2 rounded, and what that misses of exp(-g): l = -g - t ln 2 (ln 2
+//   in two parts); exp(-g) = 2^-t (1 + l), |l| < 2^-17; the hardware's 2^x and
+//   reciprocal are good to one step, the reciprocal is refined once.
+constexpr float SILU_NEAR = 87.0f;
+__device__ __forceinline__ float silu_near(float g)
+{
+    const float t = g * -0x1.715476p+0f;
+    const float l = fmaf(0x1.05c61p-29f, t, fmaf(-0x1.62e43p-1f, t, -g));
+    const float z = __builtin_amdgcn_exp2f(t);
+    const float d = 1.0f + fmaf(z, l, z);
+    const float r = __builtin_amdgcn_rcpf(d);
+    return g * fmaf(fmaf(-d, r, 1.0f), r, r);
+}
+// Beyond it the sum would overflow or round to 1: exp(g) itself, down to its
+// subnormal values, which the hardware's instructions do not return.
+__device__ __forceinline__ float silu_far(float g) { return g < 0.f ? g * expf(g) : g; }
+
 // A thread holds eight elements of a line of x as 16-byte pieces, one of bf16 or
 // two of fp32; the pieces of 16 (or 64) lanes side by side are what one load
 // instruction reads, so each uses the cache lines it touches whole. Element j
@@ -153,12 +173,17 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
         const uint8_t *p = (const uint8_t *)args.x + (row * args.ldx + c) * ES;
         float x[8];
         load8<BF16, VEC>(p, lane, 64, valid, x);
-        if constexpr (GATED) { // silu(gate) up; the reciprocal is good to 1 ulp, a division would take ten instructions
+        if constexpr (GATED) { // silu(gate) up
             float up[8];
             load8<BF16, VEC>(p + (int64_t)args.k * ES, lane, 64, valid, up);
+            float most = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                x[i] = x[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) * up[i];
+                most = fmaxf(most, fabsf(x[i]));
+            const bool far = __builtin_amdgcn_ballot_w64(most > SILU_NEAR) != 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = (far && fabsf(x[i]) > SILU_NEAR ? silu_far(x[i]) : silu_near(x[i])) * up[i];
         }
 #pragma unroll
         for (int j = 0; j < 8; j += N) {

@@ -95,3 +95,31 @@ def test_sigmoid_gradient_of_experts_that_are_closed(pts, m, experts, renorm):
     same = pts.moe_route_backward(dw, torch.nan_to_num(x, nan=0.0, neginf=-float("inf")).to(DEV), r.ids, score="sigmoid",
                                   renormalize=renorm)
     assert torch.equal(dx, same) and torch.all(dx[::2, 3] == 0) and torch.all(dx[1::2, 5] == 0)
+
+
+# ---- quantisation ------------------------------------------------------------------
+
+@pytest.mark.parametrize("low,high", [(-4.0, 4.0), (-87.0, -40.0), (40.0, 87.0), (-88.7, -87.3), (-100.0, -88.7)])
+@pytest.mark.parametrize("up", [1e3, 3e30])
+def test_gate_far_from_zero(pts, low, high, up):
+    """The gated value in fp32, seen through the scale of blocks that hold one value each."""
+    m, blocks = 40, 9
+    rng = np.random.default_rng(int(abs(high)))
+    x = np.zeros((m, 2, blocks, 128), dtype=np.float32)
+    at = rng.integers(0, 128, (m, blocks))
+    rows, cols = np.arange(m)[:, None], np.arange(blocks)[None, :]
+    x[rows, 0, cols, at] = g = rng.uniform(low, high, (m, blocks)).astype(np.float32)
+    x[rows, 1, cols, at] = v = (up * rng.uniform(1, 2, (m, blocks))).astype(np.float32)
+    q, s = pts.quantize_fp8(torch.from_numpy(x.reshape(m, -1)).to(DEV), swiglu=True)
+    g, v = g.astype(np.float64), v.astype(np.float64)
+    z = np.exp(-np.abs(g))
+    h = np.where(g < 0, g * z, g) / (1 + z) * v
+    # exp is good to a step: 2 u of z, or 2^-149; then 1 + z (2 u at most, as z <= 1), g z, the division, the product with
+    # `up` and the scale's division: 8 u
+    tol = (8 * u + np.where(g < 0, np.maximum(2.0 ** -149 / z - 2 * u, 0), 0)) * 1.001
+    want = np.abs(h) / 448
+    clear = want * (1 - tol) > 2.0 ** -126             # below, the scale is its least value
+    assert clear.mean() > (0.9 if up > 1e4 or low > -88 else -1)
+    assert np.all(np.abs(_f64(s) - want)[clear] <= (tol * want)[clear])
+    codes = R.decode(q).reshape(m, blocks, 128)
+    assert np.all(codes[rows, cols, at][clear] == (448 * np.sign(h))[clear])
