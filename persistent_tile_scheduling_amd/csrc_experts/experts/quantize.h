@@ -67,6 +67,13 @@ template <int N> __device__ __forceinline__ void quantize(const float *x, float 
         out[i / 4] = pack4(t[i], t[i + 1], t[i + 2], t[i + 3]);
 }
 
+// A word of codes of which the first `valid` lie inside the row: the others are
+// padding, 0 (a block that is not finite makes NaN codes of the zeros there).
+__device__ __forceinline__ uint32_t codes_up_to(uint32_t word, int valid)
+{
+    return valid >= 4 ? word : valid <= 0 ? 0u : word & ((1u << (8 * valid)) - 1u);
+}
+
 // silu(g) = g / (1 + exp(-g)) in fp32. Up to |g| = 87, to 6 2^-24 of its value
 // (the compiler's expf and division, to 5, made the gated form of 8192 x 7000
 // 77 us instead of 62):
@@ -200,6 +207,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
             const int e = element<BF16>(lane, j, 64);
             if (e < room) { // q's rows are padded to whole 16-byte pieces
                 uint8_t *const q = args.q + row * args.ldq + c + e;
+#pragma unroll
+                for (int w = 0; w < N / 4; ++w)
+                    codes[w] = codes_up_to(codes[w], valid - e - 4 * w);
                 if constexpr (BF16)
                     __builtin_nontemporal_store((uint64_t)codes[1] << 32 | codes[0], (uint64_t *)q);
                 else
@@ -304,9 +314,13 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeArgs a
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 32 + tid / 8, piece = (tid & 7) * 2;
-        if (r < vm && piece * 8 < room) // q's rows are padded to whole 16-byte pieces
-            __builtin_nontemporal_store(*(const u32x4 *)(codes + place(r, piece)),
-                                        (u32x4 *)(args.q + (int64_t)(row0 + r) * args.ldq + col0 + piece * 8));
+        if (r < vm && piece * 8 < room) { // q's rows are padded to whole 16-byte pieces
+            u32x4 v = *(const u32x4 *)(codes + place(r, piece));
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                v[w] = codes_up_to(v[w], vk - piece * 8 - 4 * w);
+            __builtin_nontemporal_store(v, (u32x4 *)(args.q + (int64_t)(row0 + r) * args.ldq + col0 + piece * 8));
+        }
     }
     if constexpr (SQUARE) {
         if (tid == 0)

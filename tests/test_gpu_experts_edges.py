@@ -15,6 +15,7 @@ from tests import gpu_util as U
 
 pytestmark = pytest.mark.gpu
 DEV = U.DEV
+BF16, F32 = torch.bfloat16, torch.float32
 u = 2.0 ** -24
 
 
@@ -123,3 +124,24 @@ def test_gate_far_from_zero(pts, low, high, up):
     assert np.all(np.abs(_f64(s) - want)[clear] <= (tol * want)[clear])
     codes = R.decode(q).reshape(m, blocks, 128)
     assert np.all(codes[rows, cols, at][clear] == (448 * np.sign(h))[clear])
+
+
+@pytest.mark.parametrize("k", [300, 129, 7, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("form", ["rows", "gated", "across", "square", "square across"])
+def test_padding_is_zero_beside_a_block_that_is_not_finite(pts, k, bad, dtype, form):
+    """The codes between k and the next multiple of 16 are written as 0, also where their block's codes are NaN."""
+    m, ldq, wide = 130, 320, -(-k // 16) * 16
+    x = torch.randn((m, 2 * k if form == "gated" else k), generator=torch.Generator().manual_seed(k)).to(dtype)
+    x[m - 1, k - 1] = x[0, k - 1] = bad
+    across, square = "across" in form, "square" in form
+    dev = x.t().contiguous().to(DEV) if across else x.to(DEV)
+    q = torch.full((m, ldq), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.empty((m, 3), device=DEV)
+    pts.pts_quantize_fp8(dev, 0 if dtype == BF16 else 1, 1 if across else 0, m, k, dev.shape[1], 128 if square else 1,
+                         int(form == "gated"), q, ldq, s, 3, 1)
+    torch.cuda.synchronize()
+    first = (k - 1) // 128 * 128
+    assert torch.all(q[m - 1, first:k] & 0x7F == 0x7F) and torch.all(q[0, first:k] & 0x7F == 0x7F)
+    assert torch.all(q[:, k:wide] == 0) and torch.all(q[:, wide:] == 0x55)
