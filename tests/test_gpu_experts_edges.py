@@ -1,8 +1,9 @@
 """GPU tests of the routed-experts operators where they go wrong most easily: scores near their
-limits.
+limits, gates far from zero, blocks that are not finite, workgroups that take a second tile, and
+operands past 4 GB whose rows all differ.
 
-The references are 64-bit. Tolerances are stated where they are used, in units u = 2^-24, half a
-step of fp32 relative to the value.
+The references are 64-bit; those of large products are computed on the device. Tolerances are
+stated where they are used, in units u = 2^-24, half a step of fp32 relative to the value.
 """
 from __future__ import annotations
 
@@ -12,10 +13,11 @@ import torch
 
 from tests import experts_reference as R
 from tests import gpu_util as U
+from tests.test_gpu_experts import _expert_inputs, _operand, _scale
 
 pytestmark = pytest.mark.gpu
 DEV = U.DEV
-BF16, F32 = torch.bfloat16, torch.float32
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 u = 2.0 ** -24
 
 
@@ -145,3 +147,162 @@ def test_padding_is_zero_beside_a_block_that_is_not_finite(pts, k, bad, dtype, f
     first = (k - 1) // 128 * 128
     assert torch.all(q[m - 1, first:k] & 0x7F == 0x7F) and torch.all(q[0, first:k] & 0x7F == 0x7F)
     assert torch.all(q[:, k:wide] == 0) and torch.all(q[:, wide:] == 0x55)
+
+
+# ---- products ------------------------------------------------------------------------
+
+_TABLE = torch.from_numpy(R.E4M3)
+
+
+def _values64(codes, scale):
+    """What codes and block scales stand for, on the device in 64 bits."""
+    m, k = codes.shape
+    v = _TABLE.to(DEV)[codes.contiguous().view(torch.uint8).int()]
+    s = scale.double()
+    if s.shape[0] != m:
+        s = s.repeat_interleave(128, 0)[:m]
+    return v * s.repeat_interleave(128, 1)[:, :k]
+
+
+def _check(d, a, sa, b, sb, what):
+    """|d - A . B| against the bound of tests/experts_reference.py (product_bound), all on the device."""
+    x, y = _values64(a, sa), _values64(b, sb)
+    k = x.shape[1]
+    want, mag = x @ y.t(), x.abs() @ y.abs().t()
+    bound = (128 + 2 + -(-k // 128) + 7) * u * mag
+    if d.dtype == BF16:
+        largest = torch.zeros_like(want)
+        xa, ya = x.abs(), y.abs()
+        for k0 in range(0, k, 8):
+            most = torch.zeros_like(want)
+            for i in range(k0, min(k0 + 8, k)):
+                most = torch.maximum(most, xa[:, i:i + 1] * ya[:, i])
+            largest += most
+        bound = bound + 7 * 2.0 ** -13 * largest
+        bound = bound + (want.abs() + bound) * 2.0 ** -8
+    worst = float(((d.double() - want).abs() / bound.clamp(min=1e-300)).max())
+    U.log(f"{what}: worst error / bound = {worst:.3f}")
+    assert worst <= 1, what                            # false for a NaN too
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [
+    (3100, 3300, 300, F32),         # 650 tiles of 128 x 128, two of which share a compute unit
+    (2810, 3000, 300, BF16),        # 528 of them
+    (2816, 3000, 640, BF16),
+    (4500, 4400, 300, BF16),        # 324 tiles of 256 x 256
+    (4500, 4404, 1024, BF16),
+    (4352, 4608, 130, BF16),
+])
+@pytest.mark.parametrize("rows", [False, True])
+def test_workgroups_that_take_a_second_tile(pts, m, n, k, dtype, rows):
+    """More tiles than workgroups on 256 compute units, ragged and whole extents and k blocks."""
+    U.log(f"product {m}x{n}x{k} rows {rows} {dtype}")
+    kb = -(-k // 128)
+    a, b = _operand(m, k, 1 + m), _operand(n, k, 2 + n)
+    sa, sb = _scale(m, kb, 3), _scale(n if rows else -(-n // 128), kb, 4, rows)
+    back = torch.full((m + 1, n + 8), 9.0, dtype=dtype, device=DEV)
+    d = pts.gemm_fp8(a, sa, b, sb, out=back[:m, :n])
+    _check(d, a, sa, b, sb, f"{m}x{n}x{k}")
+    assert torch.all(back[m:] == 9.0) and torch.all(back[:, n:] == 9.0)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n,k", [(4400, 300), (4608, 256)])
+def test_experts_whose_workgroups_take_a_second_tile(pts, n, k, gather):
+    sizes = [600, 0, 300, 900, 257, 256, 255, 0, 100, 1500]     # 20 tile rows of 18
+    U.log(f"experts {sizes} n {n} k {k} gather {gather}")
+    a, sa, b, sb, offsets, rows, m = _expert_inputs(sizes, n, k, 41, behind=5, gather=gather, before=2)
+    out = torch.full((m, n), 9.0, dtype=BF16, device=DEV)
+    pts.gemm_fp8_experts(a, sa, b, sb, offsets, rows, out=out)
+    o = offsets.cpu().tolist()
+    for e in range(len(sizes)):
+        if sizes[e]:
+            pick = (rows[o[e]:o[e + 1]] if gather else torch.arange(o[e], o[e + 1], device=DEV)).long()
+            _check(out[o[e]:o[e + 1]], a.view(torch.uint8)[pick].view(E4M3), sa[pick], b[e], sb[e], f"expert {e}")
+    assert torch.all(out[:o[0]] == 9.0) and torch.all(out[o[-1]:] == 9.0)
+
+
+@pytest.mark.parametrize("m,n,bad", [(4, 150, 2), (40, 150, 17), (200, 150, 127), (2000, 2100, 128),
+                                     (4100, 4000, 255)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [False, True])
+def test_nan_stays_in_its_row_and_column(pts, m, n, bad, dtype, rows):
+    """A NaN code, in the ragged last k block, and a NaN scale reach their own row or columns and nothing else, in every
+    kernel of both result types."""
+    U.log(f"NaN in {m}x{n} {dtype} rows {rows}")
+    k = 300
+    a, b = _operand(m, k, 1), _operand(n, k, 2)
+    a.view(torch.uint8)[bad, 299] = 0x7F
+    sa, sb = _scale(m, 3, 3), _scale(n if rows else -(-n // 128), 3, 4, False)
+    d = torch.isnan(pts.gemm_fp8(a, sa, b, sb, dtype))
+    assert torch.all(d[bad]) and not torch.any(d[:bad]) and not torch.any(d[bad + 1:])
+    sb[1, 0] = float("nan")
+    d = torch.isnan(pts.gemm_fp8(a, sa, b, sb, dtype))
+    at = torch.zeros(n, dtype=torch.bool, device=DEV)
+    at[1:2] = rows
+    at[128:256] |= not rows
+    assert torch.all(d[:, at]) and torch.all(d[bad])
+    assert not torch.any(d[:bad, ~at]) and not torch.any(d[bad + 1:, ~at])
+
+
+# ---- operands past 4 GB ----------------------------------------------------------------
+
+def test_rows_past_four_gigabytes_are_the_right_ones(pts):
+    """Rows that repeat with a period of 8191, so that an offset short of 2^31 or 2^32 bytes or elements names another row:
+    the quantiser's two directions, the product, and the combination with its gradients against their definitions."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    k, n, m = 4096, 2048, (1 << 20) + (1 << 17) + 5
+    part = torch.randn((8191, k), generator=torch.Generator(DEV).manual_seed(1), device=DEV).to(BF16)
+    x = part[torch.arange(m, device=DEV) % 8191]        # 9.7 GB
+    some = torch.cat([torch.arange(at - 4, at + 4) for at in (1 << 18, 1 << 19, 1 << 20, m - 4)]).to(DEV)
+    U.log(f"quantise {m} x {k}")
+    q, s = pts.quantize_fp8(x)
+    want_q, want_s = R.quantize(x[some].float().cpu().numpy(), 1)
+    assert np.array_equal(R.decode(q.view(torch.uint8)[some]), want_q)
+    assert np.array_equal(s[some].cpu().numpy(), want_s)
+    U.log("and its transpose")
+    qt, st = pts.quantize_fp8(x.t())
+    for at in (1 << 19, 1 << 20, m - 5):                # blocks of 128 rows of x, the last one of 5
+        want_q, want_s = R.quantize(x[at:at + 128, :200].t().float().cpu().numpy(), 1)
+        assert np.array_equal(R.decode(qt[:200, at:at + 128]), want_q)
+        assert np.array_equal(st[:200, at // 128].cpu().numpy(), want_s[:, 0])
+    del qt, st, x
+    U.log("product with an A and a result of 4.8 GB")
+    w, ws = pts.quantize_fp8(torch.randn((n, k), generator=torch.Generator(DEV).manual_seed(2), device=DEV), (128, 128))
+    d = pts.gemm_fp8(q, s, w, ws, BF16)
+    _check(d[some], q.view(torch.uint8)[some].view(E4M3), s[some], w, ws, "rows on both sides of the limits")
+    U.log("combination of rows of 4.8 GB")
+    positions = some.flip(0).view(-1, 4).int()
+    weights = torch.rand(positions.shape, device=DEV)
+    out = pts.moe_combine(d, weights, positions)
+    y, wt = d[some.flip(0)].double().view(-1, 4, n), weights.double().unsqueeze(2)
+    tol = 5 * u * (wt * y).abs().sum(1)
+    want = (wt * y).sum(1)
+    assert torch.all((out.double() - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8)
+    dout = torch.randn(out.shape, device=DEV).to(BF16)
+    dy, dweights = pts.moe_combine_backward(dout, d, weights, positions)
+    want = (wt * dout.double().unsqueeze(1)).view(-1, n)
+    assert torch.all((dy[some.flip(0)].double() - want).abs() <= want.abs() * (2.0 ** -8 * (1 + 2.0 ** -10)))
+    prod = y * dout.double().unsqueeze(1)
+    assert torch.all((dweights.double() - prod.sum(2)).abs() <= (n / 256 + 16) * u * prod.abs().sum(2))
+
+
+def test_experts_past_four_gigabytes_are_the_right_ones(pts):
+    """80 experts of 64 MB, all different: the first, the ones on both sides of 2^30, 2^31 and 2^32 bytes, and the last."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    e, n, k = 80, 8192, 8192
+    g = torch.Generator(DEV).manual_seed(3)
+    b = torch.empty((e, n, k), dtype=torch.uint8, device=DEV)
+    for i in range(e):
+        v = torch.randint(0, 256, (n, k), generator=g, dtype=torch.uint8, device=DEV)
+        b[i] = torch.where(v & 0x7F == 0x7F, 0, v)
+    b = b.view(E4M3)
+    sb = torch.rand((e, n // 128, k // 128), generator=g, device=DEV) + 0.5
+    a, sa = pts.quantize_fp8(torch.randn((e, k), generator=g, device=DEV))
+    offsets = torch.arange(e + 1, dtype=torch.int32, device=DEV)
+    for dtype in (BF16, F32):
+        d = pts.gemm_fp8_experts(a, sa, b, sb, offsets, out_dtype=dtype)
+        for i in (0, 15, 16, 31, 32, 63, 64, 79):
+            _check(d[i:i + 1], a[i:i + 1], sa[i:i + 1], b[i], sb[i], f"expert {i} {dtype}")
