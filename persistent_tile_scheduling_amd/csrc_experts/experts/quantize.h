@@ -174,7 +174,6 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs a
     const int valid = args.k - c, room = (args.k + 15) / 16 * 16 - c;
     const int row0 = group * args.rows_per_group;
     const int rows = min(args.rows_per_group, args.m - row0);
-#pragma unroll 2
     for (int r = wave; r < rows; r += 4) {
         const int64_t row = row0 + r;
         const uint8_t *p = (const uint8_t *)args.x + (row * args.ldx + c) * ES;
