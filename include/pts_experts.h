@@ -10,7 +10,10 @@
  * streams, status codes and gemm_last_error() is as stated in pts_gemm.h: all
  * pointers are device memory of the caller on the current device, every call is
  * asynchronous on `stream`, arguments are checked before anything is launched,
- * and operands that overlap an output are not detected.
+ * and operands that overlap an output are not detected. A problem that takes 2^32
+ * threads or more in one launch (from 2^26 tokens in the router, 2^27 rows or 2^36
+ * elements in the quantiser, 2^28 columns in a product on) may be
+ * GEMM_ERR_UNSUPPORTED.
  *
  * e4m3 is the OCP 8-bit format (largest finite value 448, no infinities).
  * "fp32 scale per block" means: the value of element (i, k) is

@@ -5,15 +5,16 @@
 // one dense product, or one per expert over rows ordered by expert. The inner
 // sum of a block starts from zero in the matrix unit; the outer sum is an fp32
 // multiply-add of its result by the block's scale. The blocks are summed in
-// ascending order, one accumulator per output, so a result does not depend on
-// timing.
+// ascending order, one accumulator per output, or with few rows one for every
+// eighth block, added up in a fixed order: a result does not depend on timing.
 //
-// On MI355X: 8192^3 to bf16 430 us, 2560 TFLOP/s. The matrix unit is busy about
-// 60% of the cycles; each of its 32-cycle instructions is followed by four
-// multiply-adds (the scales), and the power limit holds the clock at 1.7 to 2.0 of
-// 2.4 GHz, so that cycles saved elsewhere come back as a lower clock. 5000 x 7000 x
-// 3000 to fp32, both operands scaled per row: 225 us, 930 TFLOP/s, bound by the
-// vector instructions (two widenings and over two scalings per 16-cycle matrix
+// On MI355X, by the clock that the card holds: 8192^3 to bf16 430 to 480 us, 2290
+// to 2560 TFLOP/s. The matrix unit is busy about 64% of the cycles; each of its
+// 32-cycle instructions is followed by four multiply-adds (the scales), and the
+// power limit holds the clock at 1.7 to 2.0 of 2.4 GHz, so that cycles saved
+// elsewhere come back as a lower clock. 5000 x 7000 x 3000 to fp32, both operands
+// scaled per row: 227 to 259 us, 810 to 925 TFLOP/s, bound by the vector
+// instructions (two widenings and over two scalings per 16-cycle matrix
 // instruction).
 #pragma once
 

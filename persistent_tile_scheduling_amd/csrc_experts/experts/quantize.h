@@ -160,9 +160,12 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(
 // workgroup walks `rows_per_group` rows of one 512-wide strip; the strip's
 // scales are collected in LDS and written together, since they are stored with
 // the rows next to each other (one k block's scales of consecutive rows are
-// what a product's tile reads). 8192 x 7000 with the gate, bf16: 55 us (5.2
-// TB/s; a large copy reaches 5.3) with 8 rows per workgroup, 7% more with 4 or 32.
-// One row of 4096: 2.7 us, the latency of one pass.
+// what a product's tile reads). 8192 x 8192 bf16: 36 to 40 us (5.0 to 5.6 TB/s; a
+// large copy reaches 5.3), fp32 60 us (5.5). 8192 x 7000 with the gate, bf16: 59 to
+// 65 us (4.4 to 4.9 TB/s; 55 to 59 with the fast exponential, whose error grows
+// with the gate: the gate's instructions count beside the loads) with 8 rows per
+// workgroup; 4 take 3 to 6% more, 32 7%, 16 the same. One row of 4096: 2.7 us, the
+// latency of one pass.
 template <bool BF16, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeArgs args)
 {

@@ -126,6 +126,12 @@ template <class C> gemm_status launch_tiles(pts::Fp8Args &args, int cus, void *s
 // 2048 x 8192 x 8192 128 against 141 with 128 x 128; 2048 x 4096 x 4096 (half of
 // the units) 41 with 128 x 128. Experts need more than 192 rows each (64
 // experts, 4096 x 4096: 224 rows 389 against 425, 160 rows 334 with 128 x 128).
+// With both operands scaled per row that kernel takes all 256 registers and keeps
+// 24 bytes per lane in scratch; it still is the faster one but at ragged sizes
+// (8192^3 515 against 608, 4096^3 70 against 80, 2048 x 8192 x 8192 132 against
+// 152, 5000 x 7000 x 3000 150 against 142). The average is all that the host knows
+// of the experts' loads: where a few have most of the rows, the tiles fit it and
+// not them.
 // For fp32 results, whose widened operands keep the vector units busy, 128 x 128
 // is as good or better throughout (4096 x 8192 x 8192: 603 against 665 with 256 x
 // 128): two independent workgroups per compute unit hide each other's waits.

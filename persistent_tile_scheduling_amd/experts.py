@@ -427,7 +427,7 @@ def moe_fp8(x: torch.Tensor, logits: torch.Tensor, k: int, gate_up: torch.Tensor
     """A layer of routed experts: each token's ``k`` experts' outputs
     ``down_e . (silu(gate_e x) * (up_e x))``, weighted and added.
 
-    ``x``: (tokens, hidden) bf16; ``gate_up``: (experts, 2 inner, hidden) and
+    ``x``: (tokens, hidden) bf16 or fp32 (the result is bf16); ``gate_up``: (experts, 2 inner, hidden) and
     ``down``: (experts, hidden, inner), e4m3 with 128 x 128 scales; ``routing``:
     keywords of :func:`moe_route`. Eight launches at most and no host
     synchronisation.

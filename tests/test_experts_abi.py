@@ -212,3 +212,9 @@ def test_reference_rounding_matches_an_exhaustive_search():
     assert np.array_equal(np.abs(np.abs(v) - np.abs(got)), d.min(1))
     ties = np.abs(R.nearest_e4m3(mid))
     assert np.all(np.isin(ties, grid[::2]))
+
+
+def test_more_than_one_launch_holds_is_refused(pts):
+    m, k = 2 ** 31 - 2048, 2 ** 17                      # 2^34 blocks of 128 x 128
+    change = dict(m=m, k=k, ldx=k, ldq=k, block=128)
+    _refused(pts, lambda: pts.pts_quantize_fp8(*{**QUANTIZE, **change}.values(), stream=0), 2, "too large")
