@@ -14,7 +14,8 @@
 // and weight 0. A row whose softmax is not a number goes by its logits.
 //
 // Latency and instruction bound: 16384 tokens x 128 experts, 8 each, fp32 (10 MB
-// in all, 2 us of memory time): choice 8.6 us, counts 3.3, order 7.4, gradient 8.2.
+// in all, 2 us of memory time): choice 8.6 us, counts 3.3, order 7.4, gradient 9.5 (8.2 with its differences
+// taken of whole sums, which loses the gradient of a score near one).
 // One token of 256 experts with groups: 7.3 us in one launch.
 #pragma once
 
@@ -494,14 +495,33 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs args)
 // ---- gradient -----------------------------------------------------------------
 
 // dL/dx from dL/dw, for the chosen experts of `ids` (the choice itself has no
-// gradient; the bias only takes part in the choice):
-//   renormalised:  dL/dp_j = scale / S (dw_j - sum_i dw_i p_i / S), S = sum p + 1e-20
+// gradient; the bias only takes part in the choice). With S = sum p + 1e-20:
+//   renormalised:  dL/dp_j = scale / S (dw_j - sum_i dw_i p_i / S)
 //   otherwise:     dL/dp_j = scale dw_j
 //   softmax:       dL/dx_e = p_e (dL/dp_e - sum_j dL/dp_j p_j)
 //   sigmoid:       dL/dx_e = dL/dp_e p_e (1 - p_e)
+// As they stand, these lose the gradient of a score near one, which is as small
+// as what is left to the others: each difference is of nearly equal values. So
+// they are taken term by term:
+//   renormalised:  dw_j S - sum_i dw_i p_i = sum_i p_i (dw_j - dw_i) + 1e-20 dw_j,
+//                  and softmax's sum_j dL/dp_j p_j keeps only the part of 1e-20
+//   softmax:       dL/dx_e = p_e (dL/dp_e rest + sum_{i != e} p_i (dL/dp_e - dL/dp_i)),
+//                  rest: the sum of the scores that are not chosen
+//   sigmoid:       p (1 - p) = z / (1 + z)^2, z = exp(-|x|)
 // The scores are computed again. An id outside [0, experts) has no score. A
 // sigmoid's expert that no id names has no part in the weights: 0, also where
-// its logit is a NaN, which closes it.
+// its logit is a NaN, which closes it. An expert that several slots name gets
+// the sum; its score counts once among the others'.
+template <int SLOT> __device__ __forceinline__ int from_slot(const int (&x)[ROUTE_MAX_TOP / 16])
+{ // slot SLOT's value to every lane of its row
+    return __builtin_amdgcn_mov_dpp(x[SLOT / 16], 0x150 + SLOT % 16, 0xF, 0xF, true);
+}
+template <int SLOT> __device__ __forceinline__ float from_slot(const float (&x)[ROUTE_MAX_TOP / 16])
+{
+    return __uint_as_float(
+        (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x[SLOT / 16]), 0x150 + SLOT % 16, 0xF, 0xF, true));
+}
+
 template <int LPT, int VPL>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs args)
 {
@@ -569,34 +589,93 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
         dot += dw[q] * score[q];
     }
     sum = sum_lanes<16>(sum) + ROUTE_EPS;
-    dot = sum_lanes<16>(dot) / sum;
-    float back = 0.f;
+    dot = sum_lanes<16>(dot);
+    auto each_slot = [&](auto f) {
+        static_for<ROUTE_MAX_TOP>([&](auto slot) {
+            if (decltype(slot)::value < args.top)
+                f(slot);
+        });
+    };
+    float grad[ROUTE_MAX_TOP / 16], back; // by the slot's score; what softmax takes from every expert
+    if (args.renorm) {
 #pragma unroll
-    for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q) {
-        dw[q] = args.renorm ? (dw[q] - dot) * (args.scale / sum) : dw[q] * args.scale;
-        back += id[q] >= 0 ? dw[q] * score[q] : 0.f;
+        for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+            grad[q] = ROUTE_EPS * dw[q];
+        each_slot([&](auto slot) {
+            const float p_i = from_slot<decltype(slot)::value>(score), d_i = from_slot<decltype(slot)::value>(dw);
+#pragma unroll
+            for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+                grad[q] = fmaf(p_i, dw[q] - d_i, grad[q]);
+        });
+#pragma unroll
+        for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+            grad[q] = grad[q] / sum * (args.scale / sum);
+        back = dot * (ROUTE_EPS / sum) * (args.scale / sum);
+    } else {
+#pragma unroll
+        for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+            grad[q] = dw[q];
+        back = dot * args.scale;
+        if (!args.sigmoid) {
+            uint32_t chosen_here = 0; // bit v: expert v LPT + lane
+            float first[ROUTE_MAX_TOP / 16]; // 0: an earlier slot names the expert
+#pragma unroll
+            for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+                first[q] = 1.f;
+            each_slot([&](auto slot) {
+                const int e = from_slot<decltype(slot)::value>(id);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    chosen_here |= v * LPT + lane == e ? 1u << v : 0u;
+#pragma unroll
+                for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+                    first[q] = e == id[q] && decltype(slot)::value < q * 16 + (lane & 15) ? 0.f : first[q];
+            });
+            float rest = 0.f;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                rest += chosen_here >> v & 1 ? 0.f : p[v];
+            rest = sum_lanes<LPT>(rest);
+#pragma unroll
+            for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+                grad[q] *= rest;
+            each_slot([&](auto slot) {
+                const int e = from_slot<decltype(slot)::value>(id);
+                const float p_i = from_slot<decltype(slot)::value>(score), d_i = from_slot<decltype(slot)::value>(dw),
+                            f_i = from_slot<decltype(slot)::value>(first);
+#pragma unroll
+                for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+                    grad[q] = e == id[q] ? grad[q] : fmaf(p_i, f_i * dw[q] - first[q] * d_i, grad[q]);
+            });
+        }
+#pragma unroll
+        for (int q = 0; q < ROUTE_MAX_TOP / 16; ++q)
+            grad[q] *= args.scale;
     }
-    back = sum_lanes<16>(back);
     float dp[VPL];
+    uint32_t named = 0; // bit v: expert v LPT + lane
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
         dp[v] = 0.f;
-    static_for<ROUTE_MAX_TOP>([&](auto slot) { // each slot in turn to every lane of its row
-        constexpr int Q = decltype(slot)::value / 16, TO_ROW = 0x150 + decltype(slot)::value % 16;
-        if (decltype(slot)::value >= args.top)
-            return;
-        const int e = __builtin_amdgcn_mov_dpp(id[Q], TO_ROW, 0xF, 0xF, true);
-        const float d = __uint_as_float(
-            (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(dw[Q]), TO_ROW, 0xF, 0xF, true));
+    each_slot([&](auto slot) {
+        const int e = from_slot<decltype(slot)::value>(id);
+        const float d = from_slot<decltype(slot)::value>(grad);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            dp[v] += v * LPT + lane == e ? d : 0.f;
+        for (int v = 0; v < VPL; ++v) {
+            const bool mine = v * LPT + lane == e;
+            dp[v] += mine ? d : 0.f;
+            named |= mine ? 1u << v : 0u;
+        }
     });
     if (live) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = v * LPT + lane;
-            const float d = !args.sigmoid ? p[v] * (dp[v] - back) : dp[v] == 0.f ? 0.f : dp[v] * p[v];
+            float d = dp[v];
+            if (args.sigmoid)
+                d = named >> v & 1 ? d * p[v] : 0.f;
+            else
+                d = p[v] * (named >> v & 1 && !args.renorm ? d : d - back);
             if (e < experts) {
                 if (args.bf16)
                     ((__bf16 *)args.dlogits)[token * args.ld_d + e] = (__bf16)d;

@@ -84,6 +84,76 @@ def test_sigmoid_gradient_of_scores_near_one(pts, m, experts, k, low, high, reno
             assert abs(want[0, e] - diff) <= 1e-4 * abs(want[0, e]) + 64 * 2.0 ** -53 * 2.5 * np.abs(_f64(dw)[0]).sum() / h
 
 
+def _gradient_by_differences_of_slots(dw, x, ids, score, renorm, scale):
+    """The formula's gradient in 64 bits with every difference taken term by term, and the magnitudes of those terms:
+    1 - p as the sum of the other scores, a weight's derivative as sums of p_i (dw_s - dw_i)."""
+    dx, size = np.zeros_like(x), np.zeros_like(x)
+    for t in range(x.shape[0]):
+        if score == "sigmoid":
+            p, factor = 1 / (1 + np.exp(-x[t])), _sigmoid_slope(x[t])
+        else:
+            p = factor = R.scores(x[t], score)
+        ok = np.flatnonzero(ids[t] >= 0)
+        at, d = ids[t][ok], dw[t][ok].astype(np.float64)
+        q = p[at]
+        by, most = scale * d, scale * np.abs(d)        # the gradient by each slot's score
+        if renorm:
+            total = q.sum() + 1e-20
+            by = scale / total ** 2 * ((q[None, :] * (d[:, None] - d[None, :])).sum(1) + 1e-20 * d)
+            most = scale / total ** 2 * ((q[None, :] * (np.abs(d)[:, None] + np.abs(d)[None, :]) * (1 - np.eye(len(ok)))).sum(1) +
+                                         1e-20 * np.abs(d))
+        if score == "sigmoid":
+            np.add.at(dx[t], at, by * factor[at])
+            np.add.at(size[t], at, most * factor[at])
+            continue
+        if renorm:                                     # sum of by q: the differences cancel in pairs, the 1e-20 stays
+            back, back_most = scale / total ** 2 * 1e-20 * (d * q).sum(), scale / total ** 2 * 1e-20 * (np.abs(d) * q).sum()
+            dx[t], size[t] = -p * back, p * back_most
+            np.add.at(dx[t], at, by * q)
+            np.add.at(size[t], at, most * q)
+            continue
+        for e in range(x.shape[1]):
+            mine = at == e
+            rest = p.sum() - p[e] if p[e] < 0.5 else np.delete(p, e).sum()
+            dx[t, e] = p[e] * (by[mine].sum() * rest - (by * q)[~mine].sum())
+            size[t, e] = p[e] * (most[mine].sum() * rest + (most * q)[~mine].sum())
+    return dx, size
+
+
+@pytest.mark.parametrize("m,experts,k", [(5, 40, 4), (3, 300, 6), (2, 700, 32), (6, 30, 1), (4200, 24, 2), (4100, 120, 8),
+                                          (4097, 200, 17)])
+@pytest.mark.parametrize("lead", [0.0, 8.0, 25.0])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("twice", [False, True])
+def test_gradient_of_a_score_that_leads(pts, m, experts, k, lead, score, renorm, twice):
+    """One expert far ahead of the others: its gradient and theirs are as small as 1 - p, and as exact relative to that."""
+    if twice and k == 1:
+        pytest.skip("one slot")
+    U.log(f"gradient {m}x{experts} k {k} lead {lead} {score} renormalised {renorm} twice {twice}")
+    rng = np.random.default_rng(m + k)
+    x = rng.standard_normal((m, experts)) - (20 if score == "sigmoid" else 0)
+    ids = np.stack([rng.permutation(experts)[:k] for _ in range(m)]).astype(np.int32)
+    np.put_along_axis(x, ids[:, :1].astype(np.int64), x.max(1, keepdims=True) + lead, 1)
+    if twice:
+        ids[:, k // 2] = ids[:, (k - 1) * (m % 2)]      # another slot's, or the leading one's
+    ids[1, k - 1] = -1 if k > 1 else ids[1, k - 1]
+    x, dw = torch.from_numpy(x.astype(np.float32)), torch.from_numpy(rng.standard_normal((m, k)).astype(np.float32))
+    some = np.arange(m) if m < 100 else np.r_[:40, m - 40:m]
+    for dtype in (F32, BF16):
+        v = x.to(dtype)
+        dx = pts.moe_route_backward(dw.to(DEV), v.to(DEV), torch.from_numpy(ids).to(DEV), score=score, renormalize=renorm, scale=2.5)
+        z = _f64(v)[some]
+        want, size = _gradient_by_differences_of_slots(_f64(dw)[some], z, ids[some], score, renorm, 2.5)
+        # a softmax score: x - max rounds (its span in u), exp is good to 2 u, the sum adds 22 roundings, the division 1,
+        # numerator and denominator: 2 span + 28 u; a sigmoid's 4 u and its slope 12. Not renormalised: the rest's sum 22
+        # more, differences, products and sums 2 k + 10, times a score. Renormalised: three scores' sums, k + 3 each
+        one = 12 if score == "sigmoid" else 2 * (z.max() - z.min()) + 28
+        bound = 1.01 * (4 * one + 3 * k + 32) * u * size + 2.0 ** -140
+        if dtype == BF16:
+            bound = bound + (np.abs(want) + bound) * 2.0 ** -8
+        assert np.all(np.abs(_f64(dx)[some] - want) <= bound), dtype
+
+
 @pytest.mark.parametrize("m,experts", [(5, 40), (4200, 100)])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_sigmoid_gradient_of_experts_that_are_closed(pts, m, experts, renorm):
