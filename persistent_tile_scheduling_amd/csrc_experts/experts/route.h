@@ -14,8 +14,9 @@
 // and weight 0. A row whose softmax is not a number goes by its logits.
 //
 // Latency and instruction bound: 16384 tokens x 128 experts, 8 each, fp32 (10 MB
-// in all, 2 us of memory time): choice 8.6 us, counts 3.3, order 7.4, gradient 9.5 (8.2 with its differences
-// taken of whole sums, which loses the gradient of a score near one).
+// in all, 2 us of memory time): choice 8.6 us, counts 3.3, order 7.4, gradient 9.5
+// (8.2 with its differences taken of whole sums, which loses the gradient of a
+// score near one).
 // One token of 256 experts with groups: 7.3 us in one launch.
 #pragma once
 
