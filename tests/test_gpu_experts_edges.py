@@ -127,8 +127,6 @@ def _gradient_by_differences_of_slots(dw, x, ids, score, renorm, scale):
 @pytest.mark.parametrize("twice", [False, True])
 def test_gradient_of_a_score_that_leads(pts, m, experts, k, lead, score, renorm, twice):
     """One expert far ahead of the others: its gradient and theirs are as small as 1 - p, and as exact relative to that."""
-    if twice and k == 1:
-        pytest.skip("one slot")
     U.log(f"gradient {m}x{experts} k {k} lead {lead} {score} renormalised {renorm} twice {twice}")
     rng = np.random.default_rng(m + k)
     x = rng.standard_normal((m, experts)) - (20 if score == "sigmoid" else 0)
