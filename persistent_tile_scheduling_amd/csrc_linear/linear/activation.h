@@ -1,0 +1,141 @@
+// The activations of a linear layer and their slopes, in fp32.
+//
+// Each is good to a few steps of 2^-24 of its value (below 2^-119, where the
+// hardware's exponential comes to return 0, of that), and so is its slope, but
+// near a slope's own zero, where it is good to as many steps of one. Only the
+// left tail of gelu_tanh adds the rounding of its logistic's argument u, 2^-24 |u|.
+//
+// gelu is z Phi(z). With a = |z|, Phi(-a) = exp(-a^2 / 2) G(a), where G(a) =
+// erfcx(a / sqrt 2) / 2 falls smoothly from 1/2 like 1 / (a sqrt(2 pi)); it is a
+// polynomial of degree 9 in t = 1 / (1 + 0.35 a), without a constant term, fitted
+// here to the least relative error on Chebyshev points of t (3.2e-8; 3.3e-7 with
+// its evaluation in fp32). 1 + erf would lose the left tail to cancellation.
+#pragma once
+
+#include "device/common.h"
+
+namespace pts {
+
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+// exp(x + dx) for x <= 0 and a small dx: t = x / ln 2 rounded, and what that misses of the exponent (ln 2 in two parts).
+__device__ __forceinline__ float exp_of(float x, float dx)
+{
+    const float t = x * 0x1.715476p+0f;
+    const float l = fmaf(0x1.05c61p-29f, t, fmaf(-0x1.62e43p-1f, t, x)) + dx;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, l, e);
+}
+// 1 / d for d in [1, 2^60]: the hardware's reciprocal, refined once.
+__device__ __forceinline__ float reciprocal(float d)
+{
+    const float r = __builtin_amdgcn_rcpf(d);
+    return fmaf(fmaf(-d, r, 1.0f), r, r);
+}
+// v within [-most, most]; NaN stays.
+__device__ __forceinline__ float within(float v, float most) { return v > most ? most : v < -most ? -most : v; }
+
+// exp(-z^2 / 2) and Phi(-|z|).
+struct Normal {
+    float bell, below;
+};
+__device__ __forceinline__ Normal normal(float z)
+{
+    const float a = fabsf(within(z, 16.0f)); // beyond, both are 0
+    const float h = a * a;
+    Normal n;
+    n.bell = exp_of(-0.5f * h, -0.5f * fmaf(a, a, -h));
+    const float t = reciprocal(fmaf(0.35f, a, 1.0f));
+    float g = -0x1.ddb7c2p-6f;
+    g = fmaf(g, t, 0x1.26f8e2p-3f);
+    g = fmaf(g, t, -0x1.05f9cep-2f);
+    g = fmaf(g, t, 0x1.464764p-3f);
+    g = fmaf(g, t, -0x1.7c4432p-6f);
+    g = fmaf(g, t, 0x1.b05690p-4f);
+    g = fmaf(g, t, 0x1.eaca10p-4f);
+    g = fmaf(g, t, 0x1.1e70bep-3f);
+    g = fmaf(g, t, 0x1.1df1c6p-3f);
+    n.below = n.bell * (g * t);
+    return n;
+}
+
+// The logistic function of u and its complement's product with it: p and p (1 - p), from e = exp(-|u|), since 1 - p is
+// lost in the rounding of a p near 1. du: what u is short of its value.
+struct Logistic {
+    float p, slope;
+};
+__device__ __forceinline__ Logistic logistic(float u, float du)
+{
+    u = within(u, 128.0f); // beyond, e is 0
+    const float e = exp_of(-fabsf(u), u < 0.f ? du : -du);
+    const float r = reciprocal(1.0f + e);
+    return Logistic{u < 0.f ? e * r : r, e * r * r};
+}
+
+// 2 sqrt(2 / pi) (z + 0.044715 z^3), as a rounded value and the rest; beyond |z| = 16 its logistic is 0 or 1.
+__device__ __forceinline__ float tanh_argument(float z, float &rest)
+{
+    const float c = within(z, 16.0f), s = c * c;
+    const float f = fmaf(s, 0x1.2444f2p-4f, 0x1.988454p+0f); // 2 sqrt(2 / pi) (1 + 0.044715 s)
+    const float u = c * f;
+    rest = fmaf(c, f, -u);
+    return u;
+}
+
+template <int ACT> __device__ __forceinline__ float activate(float z)
+{
+    if constexpr (ACT == ACT_RELU)
+        return z < 0.f ? 0.f : z;
+    if constexpr (ACT == ACT_GELU)
+        return (z < 0.f ? 0.f : z) - fabsf(within(z, 16.0f)) * normal(z).below;
+    if constexpr (ACT == ACT_GELU_TANH) {
+        float rest;
+        const float u = tanh_argument(z, rest);
+        return z * logistic(u, rest).p;
+    }
+    if constexpr (ACT == ACT_SILU)
+        return z * logistic(z, 0.f).p;
+    return z;
+}
+
+template <int ACT> __device__ __forceinline__ float activation_slope(float z)
+{
+    if constexpr (ACT == ACT_RELU)
+        return z > 0.f ? 1.f : 0.f;
+    if constexpr (ACT == ACT_GELU) {
+        const Normal n = normal(z);
+        const float c = within(z, 16.0f);
+        return fmaf(c * 0x1.988454p-2f, n.bell, z > 0.f ? 1.0f - n.below : n.below); // Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi)
+    }
+    if constexpr (ACT == ACT_GELU_TANH) {
+        float rest;
+        const float u = tanh_argument(z, rest);
+        const Logistic l = logistic(u, rest);
+        const float c = within(z, 16.0f);
+        return fmaf(c * fmaf(c * c, 3.0f * 0x1.2444f2p-4f, 0x1.988454p+0f), l.slope, l.p);
+    }
+    if constexpr (ACT == ACT_SILU) {
+        const Logistic l = logistic(z, 0.f);
+        return fmaf(within(z, 128.0f), l.slope, l.p);
+    }
+    return 1.f;
+}
+
+// f(IntC<activation>{}) for an activation known at run time.
+template <class F> __device__ __forceinline__ void with_activation(int act, F &&f)
+{
+    switch (act) {
+    case ACT_RELU:
+        return f(IntC<ACT_RELU>{});
+    case ACT_GELU:
+        return f(IntC<ACT_GELU>{});
+    case ACT_GELU_TANH:
+        return f(IntC<ACT_GELU_TANH>{});
+    case ACT_SILU:
+        return f(IntC<ACT_SILU>{});
+    default:
+        return f(IntC<ACT_NONE>{});
+    }
+}
+
+} // namespace pts

@@ -1,0 +1,100 @@
+// A linear layer over few rows: each byte of the weight is used by one workgroup
+// only, so it goes straight from memory to the registers of the matrix unit.
+//
+// A workgroup has 16 columns (rows of the weight) and up to 16 MB rows of x. Its
+// eight waves take the blocks of 64 k in turn, U blocks at a time, eight
+// independent streams of loads; their sums are added in wave order through LDS.
+#pragma once
+
+#include "linear/epilogue.h"
+
+namespace pts {
+
+template <int MB, int U, class Epilogue>
+__global__ __launch_bounds__(512) void rows_kernel(const TileArgs args, const typename Epilogue::Args epi)
+{
+    constexpr int WAVES = 8;
+    __shared__ __align__(16) float part[WAVES][MB * 16][16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int col0 = blockIdx.x * 16, split = blockIdx.y;
+    const int all = (args.k + 63) / 64;
+    const int first = split * args.split_k, end = min(first + args.split_k, all);
+    const uint16_t *const b = args.b + (int64_t)min(col0 + l16, args.n - 1) * args.ldb;
+    const uint16_t *a[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        a[i] = args.a + (int64_t)min(i * 16 + l16, args.m - 1) * args.lda;
+    f32x4 acc[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = first + wave; k0 < end; k0 += WAVES * U) {
+        u32x4 x[U][2], y[U][MB][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = min(k0 + u * WAVES, end - 1); // past the end: read again, not used
+            const int last = min(7, (args.k - kb * 64 - 1) / 8);
+            const int64_t lo = (int64_t)kb * 64 + min(g, last) * 8, hi = (int64_t)kb * 64 + min(g + 4, last) * 8;
+            x[u][0] = __builtin_nontemporal_load((const u32x4 *)(b + lo));
+            x[u][1] = __builtin_nontemporal_load((const u32x4 *)(b + hi));
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                y[u][i][0] = *(const u32x4 *)(a[i] + lo);
+                y[u][i][1] = *(const u32x4 *)(a[i] + hi);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = k0 + u * WAVES;
+            if (kb >= end)
+                break;
+            const int left = args.k - kb * 64;
+            if (left < 64) { // what lies past the end of the rows is cleared in both operands
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int have = left - (g + 4 * h) * 8 - 2 * e;
+                        const uint32_t mask = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
+                        x[u][h][e] &= mask;
+#pragma unroll
+                        for (int i = 0; i < MB; ++i)
+                            y[u][i][h][e] &= mask;
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    acc[i] = Bf16::mfma(x[u][h], y[u][i][h], acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        *(f32x4 *)&part[wave][i * 16 + l16][g * 4] = acc[i];
+    barrier_lds();
+    const int row = tid >> 1, c = (tid & 1) * 8, valid = args.n - col0 - c;
+    if (row >= min(MB * 16, args.m) || valid <= 0)
+        return;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const f32x4 lo = *(const f32x4 *)&part[w][row][c], hi = *(const f32x4 *)&part[w][row][c + 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] += lo[i];
+            v[4 + i] += hi[i];
+        }
+    }
+    if (args.splits > 1) {
+        float *const p = args.part + ((int64_t)split * args.m + row) * args.part_ld + col0 + c;
+        *(f32x4 *)p = *(f32x4 *)v;
+        *(f32x4 *)(p + 4) = *(f32x4 *)(v + 4);
+        return;
+    }
+    Epilogue::run(epi, [&](auto e) { e.finish(epi, e.start(epi, 0, col0 + c, valid), 0, row, col0 + c, valid, v); });
+}
+
+} // namespace pts

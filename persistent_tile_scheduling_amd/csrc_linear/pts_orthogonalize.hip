@@ -1,0 +1,239 @@
+// Host side of pts_orthogonalize: argument checks and the chain of launches.
+#include "linear/ortho.h"
+
+#include <cmath>
+
+#include "linear/checks.h"
+
+namespace {
+
+using namespace pts;
+
+// Parts of the workspace, in bytes from its start, and the products' splits.
+struct Layout {
+    int64_t scale, gram, poly, half[2], master, part, all; // the squares' sums are first
+    int64_t ldx, lds;                                      // pitches of rows x cols and side x side matrices
+    int32_t blocks;
+    Split square, update; // A and A A (side x side), the update (rows x cols)
+    Split first;
+};
+int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+Layout layout(int64_t count, int64_t rows, int64_t cols)
+{
+    const int64_t side = std::min(rows, cols), lng = std::max(rows, cols);
+    Layout l;
+    l.ldx = pitch8(cols);
+    l.lds = pitch8(side);
+    l.first = choose_split(side, side, lng, count);
+    l.square = choose_split(side, side, side, count);
+    l.update = choose_split(rows, cols, side, count);
+    l.blocks = (int32_t)std::min<int64_t>(256, ceil_div(rows * ceil_div(cols, 8), 1024));
+    l.scale = count * l.blocks * 8;
+    l.gram = round16(l.scale + count * 8);
+    l.poly = l.gram + count * side * l.lds * 2;
+    l.half[0] = l.poly + count * side * l.lds * 2;
+    l.half[1] = l.half[0] + count * rows * l.ldx * 2;
+    l.master = l.half[1] + count * rows * l.ldx * 2;
+    l.part = l.master + count * rows * l.ldx * 4;
+    l.all = l.part + std::max({part_bytes(l.first, side, side, count), part_bytes(l.square, side, side, count),
+                               part_bytes(l.update, rows, cols, count)});
+    return l;
+}
+
+bool sizes(int64_t count, int64_t rows, int64_t cols)
+{
+    // the workspace's bytes and every product of the extents stay in 64 bits
+    return extent(count) && extent(rows) && extent(cols) && (count == 0 || rows == 0 || cols == 0 || rows * cols <= (INT64_C(1) << 48) / count);
+}
+
+// The largest |c1 t + c2 t^2| on [0, top].
+double largest(double c1, double c2, double top)
+{
+    double most = std::fabs(c1 * top + c2 * top * top);
+    if (c2 != 0.0 && -c1 / (2.0 * c2) > 0.0 && -c1 / (2.0 * c2) < top)
+        most = std::max(most, std::fabs(c1 * c1 / (4.0 * c2)));
+    return most;
+}
+// The largest |a s + b s^3 + c s^5| on [0, top]: at its end or where a + 3 b t + 5 c t^2 = 0, t = s^2.
+double reach(double a, double b, double c, double top)
+{
+    auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+    double most = p(top);
+    auto at = [&](double t) {
+        if (t > 0.0 && t < top * top)
+            most = std::max(most, p(std::sqrt(t)));
+    };
+    if (c != 0.0) {
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (d >= 0.0) {
+            at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+            at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+        }
+    } else if (b != 0.0) {
+        at(-a / (3.0 * b));
+    }
+    return most;
+}
+
+} // namespace
+
+extern "C" {
+
+int64_t pts_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols)
+{
+    if (!sizes(count, rows, cols) || count == 0 || rows == 0 || cols == 0)
+        return 0;
+    return layout(count, rows, cols).all;
+}
+
+gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64_t x_stride, int64_t count,
+                              int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, double eps,
+                              void *out, int64_t ld_out, int64_t out_stride, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    if (dtype_x != GEMM_DTYPE_F32 && dtype_x != GEMM_DTYPE_BF16)
+        return fail(GEMM_ERR_UNSUPPORTED, "x must be fp32 or bf16");
+    if (!sizes(count, rows, cols))
+        return fail(GEMM_ERR_INVALID_VALUE, "count, rows and cols must be in [0, 2^31 - 1024), count * rows * cols at most 2^48");
+    if (count > 65535)
+        return fail(GEMM_ERR_UNSUPPORTED, "%lld matrices; at most 65535", (long long)count);
+    if (std::min(rows, cols) >= 1 << 23 || cols >= (1 << 23) - 8)
+        return fail(GEMM_ERR_UNSUPPORTED, "a tile's offsets must fit in 32-bit: fewer than 2^23 - 8 columns");
+    if (steps < 1 || steps > 64)
+        return fail(GEMM_ERR_INVALID_VALUE, "steps must be in [1, 64], not %d", steps);
+    if (!(eps > 0.0))
+        return fail(GEMM_ERR_INVALID_VALUE, "eps must be above 0");
+    double top = 1.0;
+    for (int i = 0; i < steps; ++i) {
+        const double poly = largest(b, c, top * top), next = reach(a, b, c, top);
+        if (!(poly <= 128.0) || !(next <= 8.0))
+            return fail(GEMM_ERR_INVALID_VALUE, "the coefficients take singular values to %g in step %d: beyond fp16's reach",
+                        next, i + 1);
+        top = std::max(next, 1e-30);
+    }
+    const int size = dtype_x == GEMM_DTYPE_F32 ? 4 : 2;
+    if (x_stride < 0 || out_stride < 0 || (count > 1 && (x_stride > INT64_MAX / 16 / count || out_stride > INT64_MAX / 16 / count)))
+        return fail(GEMM_ERR_INVALID_VALUE, "bad strides of the stack");
+    gemm_status st;
+    if ((st = check_rows("x", x, ldx, rows * (count > 0), cols, size)) != GEMM_OK ||
+        (st = check_rows("out", out, ld_out, rows * (count > 0), cols, 2)) != GEMM_OK)
+        return st;
+    if ((st = check_workspace(workspace, workspace_bytes, pts_orthogonalize_workspace(count, rows, cols))) != GEMM_OK)
+        return st;
+    if (count == 0 || rows == 0 || cols == 0)
+        return GEMM_OK;
+
+    const Layout l = layout(count, rows, cols);
+    uint8_t *const work = (uint8_t *)workspace;
+    uint16_t *const gram = (uint16_t *)(work + l.gram), *const poly = (uint16_t *)(work + l.poly);
+    uint16_t *const half[2] = {(uint16_t *)(work + l.half[0]), (uint16_t *)(work + l.half[1])};
+    float *const master = (float *)(work + l.master);
+    const bool tall = rows > cols, x_whole = whole_rows(x, ldx, size) && x_stride * size % 16 == 0;
+    const int64_t side = std::min(rows, cols), lng = std::max(rows, cols);
+
+    NormArgs norm{};
+    norm.x = x;
+    norm.sums = (double *)work;
+    norm.scale = (double *)(work + l.scale);
+    norm.half = half[0];
+    norm.ldx = ldx;
+    norm.x_batch = x_stride;
+    norm.ldh = l.ldx;
+    norm.h_batch = rows * l.ldx;
+    norm.eps = eps;
+    norm.rows = (int32_t)rows;
+    norm.cols = (int32_t)cols;
+    norm.f32 = dtype_x == GEMM_DTYPE_F32;
+    norm.whole = x_whole;
+    norm.blocks = l.blocks;
+    if ((st = launch_grid(&norm_kernel, l.blocks, count, 256, stream, norm)) != GEMM_OK ||
+        (st = launch_grid(&start_kernel, ceil_div(rows * ceil_div(cols, 8), 1024), count, 256, stream, norm)) != GEMM_OK)
+        return st;
+
+    for (int i = 0; i < steps; ++i) {
+        uint16_t *const now = half[i & 1], *const next = half[(i & 1) ^ 1];
+        TileArgs args{};
+        args.part = (float *)(work + l.part);
+        args.batch = (int32_t)count;
+        // A = X X^T or X^T X
+        args.a = args.b = now;
+        args.lda = args.ldb = l.ldx;
+        args.a_batch = args.b_batch = rows * l.ldx;
+        args.m = args.n = (int32_t)side;
+        args.k = (int32_t)lng;
+        args.symmetric = l.first.splits == 1;
+        OrthoArgs epi{};
+        epi.half = gram;
+        epi.ldh = l.lds;
+        epi.h_batch = side * l.lds;
+        epi.alpha = 1.f / (ORTHO_SX * ORTHO_SX);
+        epi.half_scale = ORTHO_SA;
+        st = tall ? run_product<F16, COLS, COLS, OrthoEpilogue>(args, epi, l.first, stream)
+                  : run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.first, stream);
+        if (st != GEMM_OK)
+            return st;
+        // B = b A + c A A
+        args.a = args.b = gram;
+        args.lda = args.ldb = l.lds;
+        args.a_batch = args.b_batch = side * l.lds;
+        args.k = (int32_t)side;
+        args.symmetric = l.square.splits == 1;
+        epi.half = poly;
+        epi.alpha = c / (ORTHO_SA * ORTHO_SA);
+        epi.beta = b / ORTHO_SA;
+        epi.r = gram;
+        epi.r_type = R_F16;
+        epi.ldr = l.lds;
+        epi.r_batch = side * l.lds;
+        if ((st = run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.square, stream)) != GEMM_OK)
+            return st;
+        // X' = a X + B X or a X + X B (B = B^T)
+        args.a = tall ? now : poly;
+        args.b = tall ? poly : now;
+        args.lda = tall ? l.ldx : l.lds;
+        args.ldb = tall ? l.lds : l.ldx;
+        args.a_batch = tall ? rows * l.ldx : side * l.lds;
+        args.b_batch = tall ? side * l.lds : rows * l.ldx;
+        args.m = (int32_t)rows;
+        args.n = (int32_t)cols;
+        args.symmetric = 0;
+        epi = OrthoArgs{};
+        epi.alpha = 1.f / (ORTHO_SA * ORTHO_SX);
+        epi.beta = a;
+        if (i == 0) {
+            epi.r = x;
+            epi.r_scale = norm.scale;
+            epi.r_type = norm.f32 ? R_F32 : R_BF16;
+            epi.ldr = ldx;
+            epi.r_batch = x_stride;
+            epi.r_whole = x_whole;
+        } else {
+            epi.r = master;
+            epi.r_type = R_F32;
+            epi.ldr = l.ldx;
+            epi.r_batch = rows * l.ldx;
+            epi.r_whole = 1;
+        }
+        if (i + 1 < steps) {
+            epi.half = next;
+            epi.ldh = l.ldx;
+            epi.h_batch = rows * l.ldx;
+            epi.half_scale = ORTHO_SX;
+            epi.master = master;
+            epi.ldm = l.ldx;
+            epi.m_batch = rows * l.ldx;
+        } else {
+            epi.out = (uint16_t *)out;
+            epi.ldo = ld_out;
+            epi.o_batch = out_stride;
+            epi.o_whole = whole_rows(out, ld_out, 2) && out_stride % 8 == 0;
+        }
+        st = tall ? run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.update, stream)
+                  : run_product<F16, ROWS, COLS, OrthoEpilogue>(args, epi, l.update, stream);
+        if (st != GEMM_OK)
+            return st;
+    }
+    return GEMM_OK;
+}
+
+} // extern "C"
