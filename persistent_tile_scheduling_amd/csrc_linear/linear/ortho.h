@@ -91,8 +91,8 @@ struct OrthoStore {
         if (args.out != nullptr)
             put8(args.out + batch * args.o_batch + row * args.ldo + col, to_bf16(v), valid, args.o_whole);
     }
-    // The reflected result: rows row .. row + 7 of column col, of which the first `valid` exist, as columns of row col.
-    static __device__ __forceinline__ void mirror(const OrthoArgs &args, int batch, int row, int col, int, const float (&v)[8])
+    // The reflected result: rows row .. row + 7 of column col, as columns of row col.
+    static __device__ __forceinline__ void mirror(const OrthoArgs &args, int batch, int row, int col, const float (&v)[8])
     {
         *(u32x4 *)(args.half + batch * args.h_batch + col * args.ldh + row) = to_f16(v, args.half_scale);
     }

@@ -14,71 +14,87 @@ constexpr int64_t UNITS = 256; // compute units of the card: the choice, and wit
 constexpr int64_t MAX_EXTENT = INT32_MAX - 1024; // extents are rounded up to whole tiles in 32 bits
 
 struct Split {
-    int edge;   // tiles are edge x edge
-    int splits; // workgroups that share a tile's contraction
-    int per;    // k tiles (of 64) for each
+    int edge;            // tiles are edge x edge
+    int splits, per;     // workgroups that share a tile's contraction, and k tiles (of 64) for each:
+    int64_t whole, rest; //   so many tiles are not shared, so many are
 };
 
-inline Split choose_split(int64_t m, int64_t n, int64_t k, int64_t batch)
+// What a tile takes on MI355X, in us: per k tile, and for its first loads and its
+// results, alone on its compute unit and with another one of its kind (measured
+// with 256 and 512 tiles of 512, 4096 and 8192 k; the three ways the operands can
+// lie differ by 10%). So 256 x 256 tiles run at 1470 to 1590 TFLOP/s, 128 x 128 at
+// 1190 to 1260 (840 to 1060 alone), 64 x 64 at 650 to 790 (470 to 530 alone).
+struct TileCost {
+    int edge, resident;
+    double alone, paired, fixed;
+};
+constexpr TileCost TILE_COSTS[] = {{256, 1, 1.40, 1.40, 7.0}, {128, 2, 0.54, 0.87, 5.0}, {64, 2, 0.27, 0.38, 3.0}};
+constexpr double JOIN_US = 4.0, JOIN_BYTES_PER_US = 2.5e6; // a launch; a part written and read again
+
+// The tiles, and how the last round of them, which seldom fills the card, is
+// shared: whichever takes the least time by the costs above.
+inline Split choose_split(int64_t m, int64_t n, int64_t k, int64_t batch, bool symmetric)
 {
-    const int64_t nk = ceil_div(k, 64);
-    auto tiles = [&](int64_t edge) { return ceil_div(m, edge) * ceil_div(n, edge) * batch; };
-    Split s{64, 1, (int)std::max<int64_t>(nk, 1)};
-    if (20 * tiles(256) >= 11 * UNITS)
-        s.edge = 256;
-    else if (tiles(128) >= UNITS)
-        s.edge = 128;
-    else if (tiles(128) * nk >= 16 * UNITS)
-        s.edge = 128;
-    const int64_t t = tiles(s.edge), room = (s.edge == 256 ? 1 : 2) * UNITS;
-    if (t < UNITS && nk >= 16) {
-        const int64_t splits = std::max<int64_t>(1, std::min(room / t, nk / 8));
-        s.per = (int)ceil_div(nk, splits);
-        s.splits = (int)ceil_div(nk, s.per);
+    const int64_t nk = std::max<int64_t>(ceil_div(k, 64), 1);
+    Split best{};
+    double least = 1e300;
+    for (const TileCost &c : TILE_COSTS) {
+        const int64_t tm = ceil_div(m, c.edge), tn = ceil_div(n, c.edge);
+        const int64_t tiles = (symmetric ? tm * (tm + 1) / 2 : tm * tn) * batch, round = UNITS * c.resident;
+        const int64_t rest = tiles % round, whole = tiles - rest;
+        auto tile_us = [&](int64_t workgroups, int64_t per) { // of a last round
+            return workgroups == 0 ? 0.0 : c.fixed + (double)per * (workgroups <= UNITS ? c.alone : c.paired);
+        };
+        const double rounds = (double)(whole / round) * (c.fixed + (double)nk * c.paired);
+        for (int64_t splits = 1; splits <= 64 && (splits == 1 || (rest > 0 && nk >= 4 * splits && rest * splits <= round)); ++splits) {
+            const int64_t per = ceil_div(nk, splits), used = ceil_div(nk, per);
+            double us = rounds + tile_us(rest * used, per);
+            if (used > 1)
+                us += JOIN_US + (double)(rest * used * c.edge * c.edge * 4) / JOIN_BYTES_PER_US;
+            if (us < least) {
+                least = us;
+                best = used > 1 ? Split{c.edge, (int)used, (int)per, whole, rest} : Split{c.edge, 1, (int)nk, tiles, 0};
+            }
+        }
     }
-    return s;
+    return best;
 }
 
-// Partial sums of a split product, in fp32, rows of whole 8 columns.
-inline int64_t part_ld(int64_t n) { return (n + 7) / 8 * 8; }
-inline int64_t part_bytes(const Split &s, int64_t m, int64_t n, int64_t batch)
-{
-    return s.splits == 1 ? 0 : batch * s.splits * m * part_ld(n) * (int64_t)sizeof(float);
-}
+// Bytes of the shared tiles' sums.
+inline int64_t part_bytes(const Split &s) { return s.rest * s.splits * s.edge * s.edge * (int64_t)sizeof(float); }
 
 template <class C, class Epilogue>
-gemm_status launch_tiles(TileArgs &args, typename Epilogue::Args &epi, void *stream)
+gemm_status launch_tiles(TileArgs &args, typename Epilogue::Args &epi, const Split &s, void *stream)
 {
     args.tiles_m = (int32_t)ceil_div(args.m, C::BM);
     args.tiles_n = (int32_t)ceil_div(args.n, C::BN);
     const int64_t tiles = args.symmetric ? (int64_t)args.tiles_m * (args.tiles_m + 1) / 2 : (int64_t)args.tiles_m * args.tiles_n;
-    const int64_t grid = tiles * args.splits * args.batch;
+    const int64_t grid = s.whole + s.rest * s.splits;
     if (grid > INT32_MAX)
         return fail(GEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
     args.tiles = (int32_t)tiles;
+    args.whole = (int32_t)s.whole;
+    args.rest = (int32_t)s.rest;
+    args.splits = s.splits;
+    args.split_k = s.per;
     args.round = (int32_t)std::min<int64_t>(grid, UNITS * (160 * 1024 / C::LDS));
-    return launch_grid(&tile_kernel<C, Epilogue>, grid, 1, C::THREADS, stream, args, epi);
+    const gemm_status st = launch_grid(&tile_kernel<C, Epilogue>, grid, 1, C::THREADS, stream, args, epi);
+    if (st != GEMM_OK || s.rest == 0)
+        return st;
+    return launch_grid(&join_kernel<C, Epilogue>, s.rest * (C::BN / 64) * (C::BM / 8) / 4, 1, 256, stream, args, epi);
 }
 
-// One product (of a stack of them): the tiles, then the sum of a split's parts.
+// One product (of a stack of them): the tiles, then the sums of those that were shared.
 template <class T, int AF, int BF, class Epilogue>
 gemm_status run_product(TileArgs &args, typename Epilogue::Args &epi, const Split &s, void *stream)
 {
     if (args.m == 0 || args.n == 0 || args.batch == 0)
         return GEMM_OK;
-    args.splits = s.splits;
-    args.split_k = s.per;
-    args.part_ld = part_ld(args.n);
-    gemm_status st;
     if (s.edge == 256)
-        st = launch_tiles<TileConfig<256, 256, 2, 4, 2, AF, BF, T>, Epilogue>(args, epi, stream);
-    else if (s.edge == 128)
-        st = launch_tiles<TileConfig<128, 128, 2, 2, 2, AF, BF, T>, Epilogue>(args, epi, stream);
-    else
-        st = launch_tiles<TileConfig<64, 64, 2, 2, 3, AF, BF, T>, Epilogue>(args, epi, stream);
-    if (st != GEMM_OK || s.splits == 1)
-        return st;
-    return launch_grid(&join_kernel<Epilogue>, ceil_div((int64_t)args.batch * args.m * ((args.n + 7) / 8), 256), 1, 256, stream, args, epi);
+        return launch_tiles<TileConfig<256, 256, 2, 4, 2, AF, BF, T>, Epilogue>(args, epi, s, stream);
+    if (s.edge == 128)
+        return launch_tiles<TileConfig<128, 128, 2, 2, 2, AF, BF, T>, Epilogue>(args, epi, s, stream);
+    return launch_tiles<TileConfig<64, 64, 2, 2, 3, AF, BF, T>, Epilogue>(args, epi, s, stream);
 }
 
 } // namespace pts

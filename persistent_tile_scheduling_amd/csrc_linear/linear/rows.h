@@ -10,6 +10,9 @@
 
 namespace pts {
 
+// Partial sums of split rows: [split][m][rows_pitch(n)].
+__host__ __device__ inline int64_t rows_pitch(int64_t n) { return (n + 7) / 8 * 8; }
+
 template <int MB, int U, class Epilogue>
 __global__ __launch_bounds__(512) void rows_kernel(const TileArgs args, const typename Epilogue::Args epi)
 {
@@ -89,12 +92,35 @@ __global__ __launch_bounds__(512) void rows_kernel(const TileArgs args, const ty
         }
     }
     if (args.splits > 1) {
-        float *const p = args.part + ((int64_t)split * args.m + row) * args.part_ld + col0 + c;
+        float *const p = args.part + ((int64_t)split * args.m + row) * rows_pitch(args.n) + col0 + c;
         *(f32x4 *)p = *(f32x4 *)v;
         *(f32x4 *)(p + 4) = *(f32x4 *)(v + 4);
         return;
     }
     Epilogue::run(epi, [&](auto e) { e.finish(epi, e.start(epi, 0, col0 + c, valid), 0, row, col0 + c, valid, v); });
+}
+
+// The sum of the splits' sums, in their order, and the epilogue: eight columns per thread.
+template <class Epilogue>
+__global__ __launch_bounds__(256) void rows_join_kernel(const TileArgs args, const typename Epilogue::Args epi)
+{
+    const int pieces = (args.n + 7) / 8;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int row = (int)(at / pieces), col = (int)(at - (int64_t)row * pieces) * 8;
+    if (row >= args.m)
+        return;
+    const float *p = args.part + row * rows_pitch(args.n) + col;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < args.splits; ++s, p += args.m * rows_pitch(args.n)) {
+        const f32x4 lo = *(const f32x4 *)p, hi = *(const f32x4 *)(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] += lo[i];
+            v[4 + i] += hi[i];
+        }
+    }
+    const int valid = args.n - col;
+    Epilogue::run(epi, [&](auto e) { e.finish(epi, e.start(epi, 0, col, valid), 0, row, col, valid, v); });
 }
 
 } // namespace pts

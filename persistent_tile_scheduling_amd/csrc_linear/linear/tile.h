@@ -43,12 +43,13 @@ struct TileArgs {
     const uint16_t *a, *b;
     int64_t lda, ldb;           // elements, multiples of 8
     int64_t a_batch, b_batch;   // elements from one problem of a stack to the next
-    float *part;                // splits > 1: partial sums [batch][split][m][part_ld]
-    int64_t part_ld;
+    float *part;                // sums of the tiles that are split: [tile][split][BM][BN]
     int32_t m, n, k;
     int32_t tiles_m, tiles_n;
     int32_t tiles;              // per problem: tiles_m * tiles_n, or the upper triangle's
-    int32_t batch, splits, split_k; // split s sums k tiles [s * split_k, (s + 1) * split_k)
+    int32_t batch;
+    int32_t whole, rest;        // tiles of the stack that one workgroup each sums; those shared by `splits`,
+    int32_t splits, split_k;    //   of which number s sums k tiles [s * split_k, (s + 1) * split_k)
     int32_t symmetric;          // A B is symmetric: tiles on and above the diagonal, the others by reflection
     int32_t round;              // workgroups dealt to the dies at a time (static_position)
 };
@@ -236,7 +237,7 @@ struct Operand {
 };
 
 struct Tile {
-    int batch, split, row0, col0, vm, vn, k0, nk; // k0: first k tile
+    int batch, split, row0, col0, vm, vn, k0, nk; // split: the sums' place in `part`, or -1; k0: first k tile
     bool diagonal;
 };
 
@@ -251,15 +252,13 @@ __device__ __forceinline__ void tile_raster(int local, int rows, int cols, int &
     c = in / high;
 }
 
+// Tile t of the stack.
 template <class C>
 __device__ __forceinline__ Tile find_tile(const TileArgs &args, int t)
 {
     Tile tile;
-    const int work = args.tiles * args.splits;
-    tile.batch = t / work;
-    t -= tile.batch * work;
-    tile.split = t / args.tiles;
-    t -= tile.split * args.tiles;
+    tile.batch = t / args.tiles;
+    t -= tile.batch * args.tiles;
     int tm, tn;
     if (args.symmetric) {
         // The triangle folded into a rectangle: with an odd number e of tile rows (e + 1) / 2 x e, row p holding its own
@@ -278,14 +277,86 @@ __device__ __forceinline__ Tile find_tile(const TileArgs &args, int t)
     tile.vm = min(C::BM, args.m - tile.row0);
     tile.col0 = tn * C::BN;
     tile.vn = min(C::BN, args.n - tile.col0);
-    const int all = (args.k + C::BK - 1) / C::BK;
-    tile.k0 = tile.split * args.split_k;
-    tile.nk = max(0, min(args.split_k, all - tile.k0));
+    tile.split = -1;
+    tile.k0 = 0;
+    tile.nk = (args.k + C::BK - 1) / C::BK;
     return tile;
 }
 
+// A workgroup's work: a whole tile, or a split's share of one.
+template <class C>
+__device__ __forceinline__ Tile find_work(const TileArgs &args, int t)
+{
+    if (t < args.whole)
+        return find_tile<C>(args, t);
+    t -= args.whole;
+    const int split = t / args.rest, of = t - split * args.rest;
+    Tile tile = find_tile<C>(args, args.whole + of);
+    tile.split = of * args.splits + split;
+    tile.k0 = split * args.split_k;
+    tile.nk = max(0, min(args.split_k, tile.nk - tile.k0));
+    return tile;
+}
+
+// 512 results of a wave at a time, turned around through 2 KiB of LDS so that a
+// lane has eight consecutive columns of one row of W. A row's 16-byte chunks are
+// exchanged by the row's number, which spreads them over the banks.
+template <int W>
+struct Piece {
+    static constexpr int LANES = W / 8, HIGH = 64 / LANES, CHUNKS = W / 4;
+    float *out;
+    int lane, row, col; // this lane's row and first column
+    static __device__ __forceinline__ int place(int r, int c) { return r * W + ((c ^ (r & (CHUNKS - 1))) << 2); }
+    __device__ __forceinline__ void setup(uint8_t *lds, int lane_)
+    {
+        out = (float *)lds;
+        lane = lane_;
+        row = lane / LANES;
+        col = lane % LANES * 8;
+    }
+    // Rows H * HIGH to H * HIGH + HIGH - 1 of a row of 16 x 16 blocks: a lane has, of row lane % 16, four columns of each.
+    template <int H, int N>
+    __device__ __forceinline__ void turn(const f32x4 (&acc)[N], float (&v)[8]) const
+    {
+        const int l16 = lane & 15, g = lane >> 4;
+        if (l16 / HIGH == H) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                *(f32x4 *)(out + place(l16 % HIGH, 4 * j + g)) = acc[j];
+        }
+        wave_lds_exchange();
+        *(f32x4 *)v = *(const f32x4 *)(out + place(row, col / 4));
+        *(f32x4 *)(v + 4) = *(const f32x4 *)(out + place(row, col / 4 + 1));
+        wave_lds_exchange();
+    }
+    // v to row row0 + row of D, columns col0 + col on, of which vm x vn from (row0, col0) exist; reflected too: to column
+    // row0 + row as well, eight rows of one column per lane.
+    template <class E, class Args, class Start>
+    __device__ __forceinline__ void store(E e, const Args &epi, const Start &start, int batch, int row0, int col0, int vm, int vn,
+                                          float (&v)[8], bool reflected) const
+    {
+        if (row < vm && col < vn)
+            e.finish(epi, start, batch, row0 + row, col0 + col, vn - col, v);
+        if constexpr (E::MIRROR) {
+            if (!reflected)
+                return;
+            *(f32x4 *)(out + place(row, col / 4)) = *(f32x4 *)v;
+            *(f32x4 *)(out + place(row, col / 4 + 1)) = *(f32x4 *)(v + 4);
+            wave_lds_exchange();
+            const int c = lane % W, r8 = lane / W * 8;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = out[place(r8 + i, c / 4) + c % 4];
+            wave_lds_exchange();
+            if (c < vn && r8 < vm)
+                e.mirror(epi, batch, row0 + r8, col0 + c, x);
+        }
+    }
+};
+
 template <class C, class Epilogue>
-__global__ __launch_bounds__(C::THREADS, C::WAVES == 8 ? 2 : 1) void tile_kernel(const TileArgs args, const typename Epilogue::Args epi)
+__global__ __launch_bounds__(C::THREADS, 2) void tile_kernel(const TileArgs args, const typename Epilogue::Args epi)
 {
     using OpA = Operand<C::AF, C::BM>;
     using OpB = Operand<C::BF, C::BN>;
@@ -293,7 +364,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES == 8 ? 2 : 1) void tile_kernel
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const Tile tile = find_tile<C>(args, static_position(blockIdx.x, gridDim.x, args.round));
+    const Tile tile = find_work<C>(args, static_position(blockIdx.x, gridDim.x, args.round));
     const bool loads = wave < C::LOADERS;
     const uint32_t lds = lds_address(smem);
 
@@ -432,87 +503,59 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES == 8 ? 2 : 1) void tile_kernel
         }
     }
 
-    // The wave's piece of D, OUT_ROWS rows at a time through its part of LDS, so that a lane has eight consecutive
-    // columns of one row. A row's 16-byte chunks are exchanged by the row's number, which spreads them over the banks.
     const int row0 = wm * C::WTM, col0 = wn * C::WTN;
     if (row0 >= tile.vm || col0 >= tile.vn)
         return;
-    float *const out = (float *)(smem + C::STAGES * C::STAGE + wave * C::OUT_BYTES);
-    constexpr int CHUNKS = C::WTN / 4;
-    auto place = [](int r, int c) { return r * C::WTN + ((c ^ (r & (CHUNKS - 1))) << 2); };
-    const int l16 = lane & 15, g = lane >> 4;
-    const int my_row = lane / C::OUT_LANES, my_col = lane % C::OUT_LANES * 8;
-    const int vm = tile.vm - row0, vn = min(C::WTN, tile.vn - col0); // rows and columns of the piece
+    Piece<C::WTN> piece;
+    piece.setup(smem + C::STAGES * C::STAGE + wave * C::OUT_BYTES, lane);
     auto pieces = [&](auto &&store) {
         static_for<C::MI>([&](auto ii) {
             constexpr int I = decltype(ii)::value;
             static_for<16 / C::OUT_ROWS>([&](auto hh) {
                 constexpr int H = decltype(hh)::value;
-                if (l16 / C::OUT_ROWS == H) {
-#pragma unroll
-                    for (int j = 0; j < C::NI; ++j)
-                        *(f32x4 *)(out + place(l16 % C::OUT_ROWS, 4 * j + g)) = acc[I][j];
-                }
-                wave_lds_exchange();
                 float v[8];
-                *(f32x4 *)v = *(const f32x4 *)(out + place(my_row, my_col / 4));
-                *(f32x4 *)(v + 4) = *(const f32x4 *)(out + place(my_row, my_col / 4 + 1));
-                wave_lds_exchange();
+                piece.template turn<H>(acc[I], v);
                 store(v, I * 16 + H * C::OUT_ROWS);
             });
         });
     };
-    const int valid = vn - my_col; // of this lane's columns
-    if (args.splits > 1) {
-        float *const part = args.part + ((int64_t)(tile.batch * args.splits + tile.split) * args.m + tile.row0 + row0 + my_row) * args.part_ld +
-                            tile.col0 + col0 + my_col;
+    if (tile.split >= 0) {
+        float *const part = args.part + (int64_t)tile.split * (C::BM * C::BN) + (row0 + piece.row) * C::BN + col0 + piece.col;
         pieces([&](float(&v)[8], int r) {
-            if (r + my_row < vm && valid > 0) { // rows of part_ld, a multiple of 8: whole pieces
-                *(f32x4 *)(part + r * args.part_ld) = *(f32x4 *)v;
-                *(f32x4 *)(part + r * args.part_ld + 4) = *(f32x4 *)(v + 4);
-            }
+            *(f32x4 *)(part + r * C::BN) = *(f32x4 *)v;
+            *(f32x4 *)(part + r * C::BN + 4) = *(f32x4 *)(v + 4);
         });
         return;
     }
+    const int vm = tile.vm - row0, vn = tile.vn - col0; // rows and columns of the piece
     Epilogue::run(epi, [&](auto e) {
-        const auto at = e.start(epi, tile.batch, tile.col0 + col0 + my_col, valid);
+        const auto at = e.start(epi, tile.batch, tile.col0 + col0 + piece.col, vn - piece.col);
         pieces([&](float(&v)[8], int r) {
-            if (r + my_row < vm && valid > 0)
-                e.finish(epi, at, tile.batch, tile.row0 + row0 + r + my_row, tile.col0 + col0 + my_col, valid, v);
-            if constexpr (e.MIRROR) {
-                if (args.symmetric && !tile.diagonal) {
-                    // reflected: this lane takes eight rows of one column
-                    *(f32x4 *)(out + place(my_row, my_col / 4)) = *(f32x4 *)v;
-                    *(f32x4 *)(out + place(my_row, my_col / 4 + 1)) = *(f32x4 *)(v + 4);
-                    wave_lds_exchange();
-                    const int c = lane % C::WTN, r8 = lane / C::WTN * 8;
-                    float x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = out[place(r8 + i, c / 4) + c % 4];
-                    wave_lds_exchange();
-                    if (c < vn && r + r8 < vm)
-                        e.mirror(epi, tile.batch, tile.row0 + row0 + r + r8, tile.col0 + col0 + c, vm - r - r8, x);
-                }
-            }
+            piece.store(e, epi, at, tile.batch, tile.row0 + row0 + r, tile.col0 + col0, vm - r, vn, v,
+                        args.symmetric && !tile.diagonal);
         });
     });
 }
 
-// The sum of the splits' partial sums, in their order, and the epilogue: eight columns per thread.
-template <class Epilogue>
+// The tiles that were split: the sum of their parts, in their order, and the
+// epilogue. A wave has eight rows by 64 columns of a tile.
+template <class C, class Epilogue>
 __global__ __launch_bounds__(256) void join_kernel(const TileArgs args, const typename Epilogue::Args epi)
 {
-    const int pieces = (args.n + 7) / 8;
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= (int64_t)args.batch * args.m * pieces)
+    constexpr int ACROSS = C::BN / 64, WAVES = ACROSS * (C::BM / 8); // waves' pieces of a tile
+    __shared__ __align__(16) float out[4][512];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int at = blockIdx.x * 4 + wave, of = at / WAVES, in = at - of * WAVES; // WAVES is a multiple of 4
+    const Tile tile = find_tile<C>(args, args.whole + of);
+    const int row0 = in / ACROSS * 8, col0 = in % ACROSS * 64;
+    if (row0 >= tile.vm || col0 >= tile.vn)
         return;
-    const int64_t line = at / pieces;
-    const int col = (int)(at - line * pieces) * 8;
-    const int batch = (int)(line / args.m), row = (int)(line - (int64_t)batch * args.m);
-    const float *p = args.part + ((int64_t)batch * args.splits * args.m + row) * args.part_ld + col;
+    Piece<64> piece;
+    piece.setup((uint8_t *)out[wave], lane);
+    const float *p = args.part + (int64_t)of * args.splits * (C::BM * C::BN) + (row0 + piece.row) * C::BN + col0 + piece.col;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < args.splits; ++s, p += (int64_t)args.m * args.part_ld) {
+#pragma unroll 4
+    for (int s = 0; s < args.splits; ++s, p += C::BM * C::BN) {
         const f32x4 lo = *(const f32x4 *)p, hi = *(const f32x4 *)(p + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -520,8 +563,11 @@ __global__ __launch_bounds__(256) void join_kernel(const TileArgs args, const ty
             v[4 + i] += hi[i];
         }
     }
-    const int valid = args.n - col;
-    Epilogue::run(epi, [&](auto e) { e.finish(epi, e.start(epi, batch, col, valid), batch, row, col, valid, v); });
+    const int vm = tile.vm - row0, vn = tile.vn - col0;
+    Epilogue::run(epi, [&](auto e) {
+        const auto start = e.start(epi, tile.batch, tile.col0 + col0 + piece.col, vn - piece.col);
+        piece.store(e, epi, start, tile.batch, tile.row0 + row0, tile.col0 + col0, vm, vn, v, args.symmetric && !tile.diagonal);
+    });
 }
 
 } // namespace pts

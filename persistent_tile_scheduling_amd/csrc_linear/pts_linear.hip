@@ -12,26 +12,27 @@ using namespace pts;
 constexpr int64_t FEW_ROWS = 32;
 
 // Its split: a workgroup has 16 columns; a narrow layer's long rows are shared by more.
-Split split_rows(int64_t n, int64_t k)
+struct RowsSplit {
+    int splits, per;
+};
+RowsSplit split_rows(int64_t n, int64_t k)
 {
     const int64_t nk = std::max<int64_t>(ceil_div(k, 64), 1), strips = ceil_div(n, 16);
     const int64_t splits = std::max<int64_t>(1, std::min(UNITS / 2 / strips, nk / 64));
-    Split s{0, 1, (int)ceil_div(nk, splits)};
+    RowsSplit s{1, (int)ceil_div(nk, splits)};
     s.splits = (int)ceil_div(nk, s.per);
     return s;
 }
 
-Split choose(int64_t m, int64_t n, int64_t k) { return m <= FEW_ROWS ? split_rows(n, k) : choose_split(m, n, k, 1); }
-
-template <int MB, int U> gemm_status run_rows(TileArgs &args, LinearArgs &epi, const Split &s, void *stream)
+template <int MB, int U> gemm_status run_rows(TileArgs &args, LinearArgs &epi, void *stream)
 {
+    const RowsSplit s = split_rows(args.n, args.k);
     args.splits = s.splits;
     args.split_k = s.per;
-    args.part_ld = part_ld(args.n);
     const gemm_status st = launch_grid(&rows_kernel<MB, U, LinearEpilogue>, ceil_div(args.n, 16), s.splits, 512, stream, args, epi);
     if (st != GEMM_OK || s.splits == 1)
         return st;
-    return launch_grid(&join_kernel<LinearEpilogue>, ceil_div((int64_t)args.m * ((args.n + 7) / 8), 256), 1, 256, stream, args, epi);
+    return launch_grid(&rows_join_kernel<LinearEpilogue>, ceil_div((int64_t)args.m * ((args.n + 7) / 8), 256), 1, 256, stream, args, epi);
 }
 
 } // namespace
@@ -42,7 +43,11 @@ int64_t pts_linear_workspace(int64_t m, int64_t n, int64_t k)
 {
     if (!extent(m) || !extent(n) || !extent(k) || m == 0 || n == 0)
         return 0;
-    return part_bytes(choose(m, n, k), m, n, 1);
+    if (m <= FEW_ROWS) {
+        const RowsSplit s = split_rows(n, k);
+        return s.splits == 1 ? 0 : s.splits * m * rows_pitch(n) * (int64_t)sizeof(float);
+    }
+    return part_bytes(choose_split(m, n, k, 1, false));
 }
 
 gemm_status pts_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias, int32_t dtype_bias,
@@ -94,12 +99,11 @@ gemm_status pts_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, c
     epi.d_whole = whole_rows(y, ldy, size);
     epi.r_whole = residual != nullptr && whole_rows(residual, ldr, size);
     epi.z_whole = z_out != nullptr && whole_rows(z_out, ldz, 2);
-    const Split s = choose(m, n, k);
     if (m <= 16)
-        return run_rows<1, 4>(args, epi, s, stream);
+        return run_rows<1, 4>(args, epi, stream);
     if (m <= FEW_ROWS)
-        return run_rows<2, 4>(args, epi, s, stream);
-    return run_product<Bf16, ROWS, ROWS, LinearEpilogue>(args, epi, s, stream);
+        return run_rows<2, 4>(args, epi, stream);
+    return run_product<Bf16, ROWS, ROWS, LinearEpilogue>(args, epi, choose_split(m, n, k, 1, false), stream);
 }
 
 } // extern "C"

@@ -24,11 +24,11 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 Layout layout(int64_t m, int64_t n, int64_t k, int32_t activation)
 {
     Layout l;
-    l.dx = choose_split(m, k, n, 1);
-    l.dw = choose_split(n, k, m, 1);
+    l.dx = choose_split(m, k, n, 1, false);
+    l.dw = choose_split(n, k, m, 1, false);
     l.sums = activation == PTS_ACTIVATION_NONE ? 0 : round16(m * pitch8(n) * 2);
     l.part = l.sums + round16(ceil_div(m, block_rows(m, n)) * n * 4);
-    l.all = l.part + std::max(part_bytes(l.dx, m, k, 1), part_bytes(l.dw, n, k, 1));
+    l.all = l.part + std::max(part_bytes(l.dx), part_bytes(l.dw));
     return l;
 }
 

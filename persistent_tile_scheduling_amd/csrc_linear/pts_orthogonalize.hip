@@ -14,8 +14,7 @@ struct Layout {
     int64_t scale, gram, poly, half[2], master, part, all; // the squares' sums are first
     int64_t ldx, lds;                                      // pitches of rows x cols and side x side matrices
     int32_t blocks;
-    Split square, update; // A and A A (side x side), the update (rows x cols)
-    Split first;
+    Split gram_split, square_split, update_split;
 };
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 Layout layout(int64_t count, int64_t rows, int64_t cols)
@@ -24,9 +23,9 @@ Layout layout(int64_t count, int64_t rows, int64_t cols)
     Layout l;
     l.ldx = pitch8(cols);
     l.lds = pitch8(side);
-    l.first = choose_split(side, side, lng, count);
-    l.square = choose_split(side, side, side, count);
-    l.update = choose_split(rows, cols, side, count);
+    l.gram_split = choose_split(side, side, lng, count, true);
+    l.square_split = choose_split(side, side, side, count, true);
+    l.update_split = choose_split(rows, cols, side, count, false);
     l.blocks = (int32_t)std::min<int64_t>(256, ceil_div(rows * ceil_div(cols, 8), 1024));
     l.scale = count * l.blocks * 8;
     l.gram = round16(l.scale + count * 8);
@@ -35,8 +34,7 @@ Layout layout(int64_t count, int64_t rows, int64_t cols)
     l.half[1] = l.half[0] + count * rows * l.ldx * 2;
     l.master = l.half[1] + count * rows * l.ldx * 2;
     l.part = l.master + count * rows * l.ldx * 4;
-    l.all = l.part + std::max({part_bytes(l.first, side, side, count), part_bytes(l.square, side, side, count),
-                               part_bytes(l.update, rows, cols, count)});
+    l.all = l.part + std::max({part_bytes(l.gram_split), part_bytes(l.square_split), part_bytes(l.update_split)});
     return l;
 }
 
@@ -161,15 +159,15 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         args.a_batch = args.b_batch = rows * l.ldx;
         args.m = args.n = (int32_t)side;
         args.k = (int32_t)lng;
-        args.symmetric = l.first.splits == 1;
+        args.symmetric = 1;
         OrthoArgs epi{};
         epi.half = gram;
         epi.ldh = l.lds;
         epi.h_batch = side * l.lds;
         epi.alpha = 1.f / (ORTHO_SX * ORTHO_SX);
         epi.half_scale = ORTHO_SA;
-        st = tall ? run_product<F16, COLS, COLS, OrthoEpilogue>(args, epi, l.first, stream)
-                  : run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.first, stream);
+        st = tall ? run_product<F16, COLS, COLS, OrthoEpilogue>(args, epi, l.gram_split, stream)
+                  : run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.gram_split, stream);
         if (st != GEMM_OK)
             return st;
         // B = b A + c A A
@@ -177,7 +175,6 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         args.lda = args.ldb = l.lds;
         args.a_batch = args.b_batch = side * l.lds;
         args.k = (int32_t)side;
-        args.symmetric = l.square.splits == 1;
         epi.half = poly;
         epi.alpha = c / (ORTHO_SA * ORTHO_SA);
         epi.beta = b / ORTHO_SA;
@@ -185,7 +182,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         epi.r_type = R_F16;
         epi.ldr = l.lds;
         epi.r_batch = side * l.lds;
-        if ((st = run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.square, stream)) != GEMM_OK)
+        if ((st = run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.square_split, stream)) != GEMM_OK)
             return st;
         // X' = a X + B X or a X + X B (B = B^T)
         args.a = tall ? now : poly;
@@ -228,8 +225,8 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
             epi.o_batch = out_stride;
             epi.o_whole = whole_rows(out, ld_out, 2) && out_stride % 8 == 0;
         }
-        st = tall ? run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.update, stream)
-                  : run_product<F16, ROWS, COLS, OrthoEpilogue>(args, epi, l.update, stream);
+        st = tall ? run_product<F16, ROWS, ROWS, OrthoEpilogue>(args, epi, l.update_split, stream)
+                  : run_product<F16, ROWS, COLS, OrthoEpilogue>(args, epi, l.update_split, stream);
         if (st != GEMM_OK)
             return st;
     }
