@@ -39,15 +39,18 @@ __device__ __forceinline__ void put8(float *p, const float (&v)[8], int valid, b
         if (i < valid)
             p[i] = v[i];
 }
+__device__ __forceinline__ void from_bf16(const u32x4 &w, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
 __device__ __forceinline__ void get8(const uint16_t *p, float (&v)[8], int valid, bool whole)
 {
     if (whole && valid >= 8) {
-        const u32x4 w = *(const u32x4 *)p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        from_bf16(*(const u32x4 *)p, v);
         return;
     }
 #pragma unroll
@@ -66,6 +69,29 @@ __device__ __forceinline__ void get8(const float *p, float (&v)[8], int valid, b
         v[i] = i < valid ? p[i] : 0.f;
 }
 
+// Eight values as they lie in memory, loaded ahead of their use.
+struct Raw8 {
+    u32x4 lo, hi;
+};
+template <bool F32> __device__ __forceinline__ void fetch8(Raw8 &r, const void *p, int64_t at)
+{
+    if constexpr (F32) {
+        r.lo = *(const u32x4 *)((const float *)p + at);
+        r.hi = *(const u32x4 *)((const float *)p + at + 4);
+    } else {
+        r.lo = *(const u32x4 *)((const uint16_t *)p + at);
+    }
+}
+__device__ __forceinline__ void from_f32(const Raw8 &r, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(r.lo[i]);
+        v[4 + i] = __uint_as_float(r.hi[i]);
+    }
+}
+// An epilogue's store has three parts: start, once for a lane's columns; fetch, what a row's results need from memory,
+// ahead of them; finish, the results.
 struct LinearArgs {
     void *d;
     const void *bias;     // of n, or null
@@ -79,6 +105,7 @@ struct LinearArgs {
 // z = sum + bias; D = act(z) + residual.
 template <int ACT> struct LinearStore {
     static constexpr bool MIRROR = false;
+    using Raw = Raw8;
     struct Start {
         float bias[8];
     };
@@ -96,8 +123,17 @@ template <int ACT> struct LinearStore {
         }
         return s;
     }
-    static __device__ __forceinline__ void finish(const LinearArgs &args, const Start &s, int, int row, int col, int valid,
-                                                  float (&v)[8])
+    static __device__ __forceinline__ void fetch(const LinearArgs &args, int, int row, int col, int valid, Raw8 &r)
+    {
+        if (args.residual != nullptr && args.r_whole && valid >= 8) {
+            if (args.d_f32)
+                fetch8<true>(r, args.residual, row * args.ldr + col);
+            else
+                fetch8<false>(r, args.residual, row * args.ldr + col);
+        }
+    }
+    static __device__ __forceinline__ void finish(const LinearArgs &args, const Start &s, const Raw8 &fetched, int, int row,
+                                                  int col, int valid, float (&v)[8])
     {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -109,10 +145,17 @@ template <int ACT> struct LinearStore {
             v[i] = activate<ACT>(v[i]);
         if (args.residual != nullptr) {
             float r[8];
-            if (args.d_f32)
-                get8((const float *)args.residual + row * args.ldr + col, r, valid, args.r_whole);
-            else
-                get8((const uint16_t *)args.residual + row * args.ldr + col, r, valid, args.r_whole);
+            if (args.d_f32) {
+                if (args.r_whole && valid >= 8)
+                    from_f32(fetched, r);
+                else
+                    get8((const float *)args.residual + row * args.ldr + col, r, valid, false);
+            } else {
+                if (args.r_whole && valid >= 8)
+                    from_bf16(fetched.lo, r);
+                else
+                    get8((const uint16_t *)args.residual + row * args.ldr + col, r, valid, false);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] += r[i];
@@ -135,10 +178,12 @@ struct LinearEpilogue {
 // D = sum (the gradients' products).
 struct PlainStore {
     static constexpr bool MIRROR = false;
+    using Raw = Raw8;
     struct Start {};
     static __device__ __forceinline__ Start start(const LinearArgs &, int, int, int) { return {}; }
-    static __device__ __forceinline__ void finish(const LinearArgs &args, const Start &, int, int row, int col, int valid,
-                                                  float (&v)[8])
+    static __device__ __forceinline__ void fetch(const LinearArgs &, int, int, int, int, Raw8 &) {}
+    static __device__ __forceinline__ void finish(const LinearArgs &args, const Start &, const Raw8 &, int, int row, int col,
+                                                  int valid, float (&v)[8])
     {
         if (args.d_f32)
             put8((float *)args.d + row * args.ldd + col, v, valid, args.d_whole);

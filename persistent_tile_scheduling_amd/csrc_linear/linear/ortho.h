@@ -7,11 +7,15 @@
 // each of which applies p(s) = a s + b s^3 + c s^5 to the singular values.
 //
 // Precision. The products' operands are fp16 (11 bits, at bf16's rate), scaled by
-// powers of two into its range; sums are fp32. X itself is held in fp32 beside
-// its fp16 form for the term a X: small singular values grow 3.4-fold a step,
-// and a rounding of X would grow with them where X has none. Against 64 bits, five
-// steps, 512 x 512: bf16 throughout 1.0e-2 of the result on normal data and 0.22
-// on rank 32, fp16 throughout 1.3e-3 and 2.8e-2, this form 1.5e-3 and 5.8e-4.
+// powers of two into its range; sums are fp32. For the term a X, X has 8 bits more
+// beside its fp16 form, what that is short of it in e4m3: small singular values
+// grow 3.4-fold a step, and a rounding of X would grow with them where X has none.
+// In the last step it no longer would. Against 64 bits, five steps, 512 x 512, on
+// normal data and on rank 32: bf16 throughout 1.0e-2 and 0.22 of the result, fp16
+// throughout 1.3e-3 and 2.8e-2, with the rest of X in fp32 1.5e-3 and 5.8e-4, this
+// form 1.4e-3 and 1.0e-3. The rest costs a byte read and written per element and
+// step, where fp32 beside fp16 took four: the update of 12 matrices of 1024 x 4096
+// is bound by memory.
 #pragma once
 
 #include "linear/epilogue.h"
@@ -20,15 +24,19 @@ namespace pts {
 
 constexpr float ORTHO_SX = 1024.f; // X entries in fp16, times this (at most 8 before it)
 constexpr float ORTHO_SA = 256.f;  // A and B entries
+constexpr float ORTHO_SR = 512.f;  // half a step of fp16 below 2048 is at most 256 times less than one
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 struct OrthoArgs {
-    const void *r;          // added times beta: null, A (fp16), X (fp32), or x itself
+    const void *r;          // added times beta: null, a matrix of the library's (fp16), or x itself
+    const uint8_t *r_rest;  // with fp16: what it is short of its value, or null
     const double *r_scale;  // x: 1 / (|x|_F + eps), one per matrix
     uint16_t *half;         // results, those that are not null: in fp16 times half_scale,
-    float *master;          //   in fp32,
+    uint8_t *rest;          //   what that is short of its value (e4m3, times ORTHO_SR more; laid out as half),
     uint16_t *out;          //   in bf16
-    int64_t ldr, ldh, ldm, ldo;
-    int64_t r_batch, h_batch, m_batch, o_batch;
+    int64_t ldr, ldh, ldo;
+    int64_t r_batch, h_batch, o_batch;
     float alpha, beta, half_scale;
     int32_t r_type, r_whole, o_whole;
 };
@@ -49,10 +57,26 @@ __device__ __forceinline__ u32x4 to_f16(const float (&v)[8], float scale)
 // whole.
 struct OrthoStore {
     static constexpr bool MIRROR = true;
+    using Raw = Raw8;
     struct Start {};
     static __device__ __forceinline__ Start start(const OrthoArgs &, int, int, int) { return {}; }
-    static __device__ __forceinline__ void finish(const OrthoArgs &args, const Start &, int batch, int row, int col, int valid,
-                                                  float (&v)[8])
+    static __device__ __forceinline__ void fetch(const OrthoArgs &args, int batch, int row, int col, int valid, Raw8 &r)
+    {
+        const int64_t at = batch * args.r_batch + row * args.ldr + col;
+        if (args.r_type == R_F16) {
+            fetch8<false>(r, args.r, at);
+            if (args.r_rest != nullptr) {
+                const u32x2 w = *(const u32x2 *)(args.r_rest + at);
+                r.hi[0] = w[0];
+                r.hi[1] = w[1];
+            }
+        } else if (args.r_type == R_F32 && args.r_whole && valid >= 8)
+            fetch8<true>(r, args.r, at);
+        else if (args.r_type == R_BF16 && args.r_whole && valid >= 8)
+            fetch8<false>(r, args.r, at);
+    }
+    static __device__ __forceinline__ void finish(const OrthoArgs &args, const Start &, const Raw8 &fetched, int batch, int row,
+                                                  int col, int valid, float (&v)[8])
     {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -60,16 +84,31 @@ struct OrthoStore {
         if (args.r_type != R_NONE) {
             float r[8];
             const int64_t at = batch * args.r_batch + row * args.ldr + col;
+            const bool ahead = args.r_whole && valid >= 8;
             if (args.r_type == R_F16) {
-                const u32x4 w = *(const u32x4 *)((const uint16_t *)args.r + at);
-                const f16x8 h = __builtin_bit_cast(f16x8, w);
+                const f16x8 h = __builtin_bit_cast(f16x8, fetched.lo);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     r[i] = (float)h[i];
+                if (args.r_rest != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const f32x2 d = i & 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)fetched.hi[i / 4], true)
+                                              : __builtin_amdgcn_cvt_pk_f32_fp8((int)fetched.hi[i / 4], false);
+                        r[i] = fmaf(d[0], 1.f / ORTHO_SR, r[i]);
+                        r[i + 1] = fmaf(d[1], 1.f / ORTHO_SR, r[i + 1]);
+                    }
+                }
             } else if (args.r_type == R_F32) {
-                get8((const float *)args.r + at, r, valid, args.r_whole);
+                if (ahead)
+                    from_f32(fetched, r);
+                else
+                    get8((const float *)args.r + at, r, valid, false);
             } else {
-                get8((const uint16_t *)args.r + at, r, valid, args.r_whole);
+                if (ahead)
+                    from_bf16(fetched.lo, r);
+                else
+                    get8((const uint16_t *)args.r + at, r, valid, false);
             }
             if (args.r_scale != nullptr) {
                 const double s = args.r_scale[batch];
@@ -81,12 +120,24 @@ struct OrthoStore {
             for (int i = 0; i < 8; ++i)
                 v[i] = fmaf(args.beta, r[i], v[i]);
         }
-        if (args.half != nullptr)
-            *(u32x4 *)(args.half + batch * args.h_batch + row * args.ldh + col) = to_f16(v, args.half_scale);
-        if (args.master != nullptr) {
-            float *const p = args.master + batch * args.m_batch + row * args.ldm + col;
-            *(f32x4 *)p = *(f32x4 *)v;
-            *(f32x4 *)(p + 4) = *(f32x4 *)(v + 4);
+        if (args.half != nullptr) {
+            const int64_t at = batch * args.h_batch + row * args.ldh + col;
+            const u32x4 w = to_f16(v, args.half_scale);
+            *(u32x4 *)(args.half + at) = w;
+            if (args.rest != nullptr) {
+                const f16x8 h = __builtin_bit_cast(f16x8, w);
+                int word[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    float d[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        d[j] = fminf(fmaxf(fmaf(v[i + j], args.half_scale, -(float)h[i + j]) * ORTHO_SR, -448.f), 448.f);
+                    word[i / 4] = i & 2 ? __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], word[i / 4], true)
+                                        : __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], word[i / 4], false);
+                }
+                *(u32x2 *)(args.rest + at) = u32x2{(uint32_t)word[0], (uint32_t)word[1]};
+            }
         }
         if (args.out != nullptr)
             put8(args.out + batch * args.o_batch + row * args.ldo + col, to_bf16(v), valid, args.o_whole);

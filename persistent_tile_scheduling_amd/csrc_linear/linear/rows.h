@@ -97,7 +97,11 @@ __global__ __launch_bounds__(512) void rows_kernel(const TileArgs args, const ty
         *(f32x4 *)(p + 4) = *(f32x4 *)(v + 4);
         return;
     }
-    Epilogue::run(epi, [&](auto e) { e.finish(epi, e.start(epi, 0, col0 + c, valid), 0, row, col0 + c, valid, v); });
+    Epilogue::run(epi, [&](auto e) {
+        Raw8 r;
+        e.fetch(epi, 0, row, col0 + c, valid, r);
+        e.finish(epi, e.start(epi, 0, col0 + c, valid), r, 0, row, col0 + c, valid, v);
+    });
 }
 
 // The sum of the splits' sums, in their order, and the epilogue: eight columns per thread.
@@ -120,7 +124,11 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const TileArgs args, con
         }
     }
     const int valid = args.n - col;
-    Epilogue::run(epi, [&](auto e) { e.finish(epi, e.start(epi, 0, col, valid), 0, row, col, valid, v); });
+    Epilogue::run(epi, [&](auto e) {
+        Raw8 r;
+        e.fetch(epi, 0, row, col, valid, r);
+        e.finish(epi, e.start(epi, 0, col, valid), r, 0, row, col, valid, v);
+    });
 }
 
 } // namespace pts

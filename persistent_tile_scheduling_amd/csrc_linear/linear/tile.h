@@ -331,12 +331,18 @@ struct Piece {
     }
     // v to row row0 + row of D, columns col0 + col on, of which vm x vn from (row0, col0) exist; reflected too: to column
     // row0 + row as well, eight rows of one column per lane.
-    template <class E, class Args, class Start>
-    __device__ __forceinline__ void store(E e, const Args &epi, const Start &start, int batch, int row0, int col0, int vm, int vn,
-                                          float (&v)[8], bool reflected) const
+    template <class E, class Args>
+    __device__ __forceinline__ void fetch(E e, const Args &epi, int batch, int row0, int col0, int vm, int vn, typename E::Raw &raw) const
     {
         if (row < vm && col < vn)
-            e.finish(epi, start, batch, row0 + row, col0 + col, vn - col, v);
+            e.fetch(epi, batch, row0 + row, col0 + col, vn - col, raw);
+    }
+    template <class E, class Args, class Start>
+    __device__ __forceinline__ void store(E e, const Args &epi, const Start &start, const typename E::Raw &raw, int batch, int row0,
+                                          int col0, int vm, int vn, float (&v)[8], bool reflected) const
+    {
+        if (row < vm && col < vn)
+            e.finish(epi, start, raw, batch, row0 + row, col0 + col, vn - col, v);
         if constexpr (E::MIRROR) {
             if (!reflected)
                 return;
@@ -508,31 +514,42 @@ __global__ __launch_bounds__(C::THREADS, 2) void tile_kernel(const TileArgs args
         return;
     Piece<C::WTN> piece;
     piece.setup(smem + C::STAGES * C::STAGE + wave * C::OUT_BYTES, lane);
-    auto pieces = [&](auto &&store) {
-        static_for<C::MI>([&](auto ii) {
-            constexpr int I = decltype(ii)::value;
-            static_for<16 / C::OUT_ROWS>([&](auto hh) {
-                constexpr int H = decltype(hh)::value;
-                float v[8];
-                piece.template turn<H>(acc[I], v);
-                store(v, I * 16 + H * C::OUT_ROWS);
-            });
-        });
+    constexpr int HALVES = 16 / C::OUT_ROWS, PIECES = C::MI * HALVES;
+    auto turned = [&](auto i, float(&v)[8]) {
+        constexpr int I = decltype(i)::value;
+        piece.template turn<I % HALVES>(acc[I / HALVES], v);
     };
     if (tile.split >= 0) {
         float *const part = args.part + (int64_t)tile.split * (C::BM * C::BN) + (row0 + piece.row) * C::BN + col0 + piece.col;
-        pieces([&](float(&v)[8], int r) {
-            *(f32x4 *)(part + r * C::BN) = *(f32x4 *)v;
-            *(f32x4 *)(part + r * C::BN + 4) = *(f32x4 *)(v + 4);
+        static_for<PIECES>([&](auto i) {
+            float v[8];
+            turned(i, v);
+            float *const p = part + decltype(i)::value * C::OUT_ROWS * C::BN;
+            *(f32x4 *)p = *(f32x4 *)v;
+            *(f32x4 *)(p + 4) = *(f32x4 *)(v + 4);
         });
         return;
     }
     const int vm = tile.vm - row0, vn = tile.vn - col0; // rows and columns of the piece
     Epilogue::run(epi, [&](auto e) {
-        const auto at = e.start(epi, tile.batch, tile.col0 + col0 + piece.col, vn - piece.col);
-        pieces([&](float(&v)[8], int r) {
-            piece.store(e, epi, at, tile.batch, tile.row0 + row0 + r, tile.col0 + col0, vm - r, vn, v,
-                        args.symmetric && !tile.diagonal);
+        // what the pieces need from memory is on its way AHEAD pieces before
+        constexpr int AHEAD = PIECES < 4 ? PIECES : 4;
+        typename decltype(e)::Raw raw[AHEAD];
+        auto fetch = [&](auto i) {
+            constexpr int I = decltype(i)::value;
+            if constexpr (I < PIECES)
+                piece.fetch(e, epi, tile.batch, tile.row0 + row0 + I * C::OUT_ROWS, tile.col0 + col0, vm - I * C::OUT_ROWS, vn, raw[I % AHEAD]);
+        };
+        static_for<AHEAD>(fetch);
+        const auto start = e.start(epi, tile.batch, tile.col0 + col0 + piece.col, vn - piece.col);
+        static_for<PIECES>([&](auto i) {
+            constexpr int I = decltype(i)::value;
+            float v[8];
+            turned(i, v);
+            const auto mine = raw[I % AHEAD];
+            fetch(IntC<I + AHEAD>{});
+            piece.store(e, epi, start, mine, tile.batch, tile.row0 + row0 + I * C::OUT_ROWS, tile.col0 + col0, vm - I * C::OUT_ROWS,
+                        vn, v, args.symmetric && !tile.diagonal);
         });
     });
 }
@@ -552,21 +569,23 @@ __global__ __launch_bounds__(256) void join_kernel(const TileArgs args, const ty
         return;
     Piece<64> piece;
     piece.setup((uint8_t *)out[wave], lane);
-    const float *p = args.part + (int64_t)of * args.splits * (C::BM * C::BN) + (row0 + piece.row) * C::BN + col0 + piece.col;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int s = 0; s < args.splits; ++s, p += C::BM * C::BN) {
-        const f32x4 lo = *(const f32x4 *)p, hi = *(const f32x4 *)(p + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] += lo[i];
-            v[4 + i] += hi[i];
-        }
-    }
     const int vm = tile.vm - row0, vn = tile.vn - col0;
+    const float *p = args.part + (int64_t)of * args.splits * (C::BM * C::BN) + (row0 + piece.row) * C::BN + col0 + piece.col;
     Epilogue::run(epi, [&](auto e) {
+        typename decltype(e)::Raw raw;
+        piece.fetch(e, epi, tile.batch, tile.row0 + row0, tile.col0 + col0, vm, vn, raw);
         const auto start = e.start(epi, tile.batch, tile.col0 + col0 + piece.col, vn - piece.col);
-        piece.store(e, epi, start, tile.batch, tile.row0 + row0, tile.col0 + col0, vm, vn, v, args.symmetric && !tile.diagonal);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < args.splits; ++s, p += C::BM * C::BN) {
+            const f32x4 lo = *(const f32x4 *)p, hi = *(const f32x4 *)(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] += lo[i];
+                v[4 + i] += hi[i];
+            }
+        }
+        piece.store(e, epi, start, raw, tile.batch, tile.row0 + row0, tile.col0 + col0, vm, vn, v, args.symmetric && !tile.diagonal);
     });
 }
 

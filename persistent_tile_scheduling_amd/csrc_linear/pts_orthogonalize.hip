@@ -11,7 +11,7 @@ using namespace pts;
 
 // Parts of the workspace, in bytes from its start, and the products' splits.
 struct Layout {
-    int64_t scale, gram, poly, half[2], master, part, all; // the squares' sums are first
+    int64_t scale, gram, poly, half[2], rest, part, all; // the squares' sums are first
     int64_t ldx, lds;                                      // pitches of rows x cols and side x side matrices
     int32_t blocks;
     Split gram_split, square_split, update_split;
@@ -32,8 +32,8 @@ Layout layout(int64_t count, int64_t rows, int64_t cols)
     l.poly = l.gram + count * side * l.lds * 2;
     l.half[0] = l.poly + count * side * l.lds * 2;
     l.half[1] = l.half[0] + count * rows * l.ldx * 2;
-    l.master = l.half[1] + count * rows * l.ldx * 2;
-    l.part = l.master + count * rows * l.ldx * 4;
+    l.rest = l.half[1] + count * rows * l.ldx * 2;
+    l.part = l.rest + round16(count * rows * l.ldx);
     l.all = l.part + std::max({part_bytes(l.gram_split), part_bytes(l.square_split), part_bytes(l.update_split)});
     return l;
 }
@@ -125,7 +125,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
     uint8_t *const work = (uint8_t *)workspace;
     uint16_t *const gram = (uint16_t *)(work + l.gram), *const poly = (uint16_t *)(work + l.poly);
     uint16_t *const half[2] = {(uint16_t *)(work + l.half[0]), (uint16_t *)(work + l.half[1])};
-    float *const master = (float *)(work + l.master);
+    uint8_t *const rest = work + l.rest;
     const bool tall = rows > cols, x_whole = whole_rows(x, ldx, size) && x_stride * size % 16 == 0;
     const int64_t side = std::min(rows, cols), lng = std::max(rows, cols);
 
@@ -196,8 +196,8 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         args.symmetric = 0;
         epi = OrthoArgs{};
         epi.alpha = 1.f / (ORTHO_SA * ORTHO_SX);
-        epi.beta = a;
         if (i == 0) {
+            epi.beta = a;
             epi.r = x;
             epi.r_scale = norm.scale;
             epi.r_type = norm.f32 ? R_F32 : R_BF16;
@@ -205,20 +205,19 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
             epi.r_batch = x_stride;
             epi.r_whole = x_whole;
         } else {
-            epi.r = master;
-            epi.r_type = R_F32;
+            epi.beta = a / ORTHO_SX;
+            epi.r = now;
+            epi.r_rest = i + 1 < steps ? rest : nullptr;
+            epi.r_type = R_F16;
             epi.ldr = l.ldx;
             epi.r_batch = rows * l.ldx;
-            epi.r_whole = 1;
         }
         if (i + 1 < steps) {
             epi.half = next;
             epi.ldh = l.ldx;
             epi.h_batch = rows * l.ldx;
             epi.half_scale = ORTHO_SX;
-            epi.master = master;
-            epi.ldm = l.ldx;
-            epi.m_batch = rows * l.ldx;
+            epi.rest = i + 2 < steps ? rest : nullptr;
         } else {
             epi.out = (uint16_t *)out;
             epi.ldo = ld_out;

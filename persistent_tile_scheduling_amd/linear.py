@@ -249,7 +249,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     ``x``: (rows, cols), or (count, rows, cols): a stack of matrices, each by
     itself; bf16 or fp32, rows or columns contiguous. ``out``: bf16, of ``x``'s shape,
     written in place when given, must not share memory with ``x`` (not checked).
-    The products are of fp16 operands, the matrix itself is held in fp32; the
+    The products are of fp16 operands, the matrix itself has eight bits more; the
     coefficients must keep the singular values of [0, 1] below 8 (5 steps of the
     defaults: 1.2).
     """

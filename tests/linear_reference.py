@@ -92,7 +92,8 @@ def check(got, want, bound, what=""):
 
 
 def orthogonalize(x, steps=5, coefficients=QUINTIC, eps=1e-7, rounded=False):
-    """The steps in 64 bits; rounded: with the kernel's roundings, of the products' operands to fp16."""
+    """The steps in 64 bits; rounded: with the kernel's roundings, of the products' operands to fp16 and of the matrix to
+    fp16 and what that is short of it in e4m3 (to fp16 alone before the last step)."""
     a, b, c = coefficients
     x = x.double()
     x = x / (x.square().sum((-1, -2), keepdim=True).sqrt() + eps)
@@ -101,11 +102,13 @@ def orthogonalize(x, steps=5, coefficients=QUINTIC, eps=1e-7, rounded=False):
     def half(v, scale):
         return (v * scale).half().double() / scale if rounded else v
 
-    for _ in range(steps):
+    for i in range(steps):
         h = half(x, 1024.0)
         gram = half(h.transpose(-1, -2) @ h if tall else h @ h.transpose(-1, -2), 256.0)
         poly = half(b * gram + c * (gram @ gram), 256.0)
         x = a * x + (h @ poly if tall else poly @ h)
-        if rounded:
-            x = x.float().double()
+        if rounded and i + 1 < steps:
+            whole = half(x, 1024.0)
+            rest = ((x - whole) * 2.0 ** 19).clamp(-448, 448).to(torch.float8_e4m3fn).double() / 2.0 ** 19
+            x = whole + rest if i + 2 < steps else whole
     return x
