@@ -8,31 +8,58 @@ namespace {
 
 using namespace pts;
 
-// Up to 32 rows go without LDS (rows_kernel).
+// Up to 32 rows go without LDS (rows_kernel). A compute unit has some 130 cache
+// lines on their way to it, 20 GB/s from memory, so what counts is that all of
+// them load: a narrow layer's long rows are split over the workgroups, as far as
+// one pass of a workgroup's waves covers a share (24 x 1000 x 8192: 16.2 us in 2
+// shares, 11.9 in 8, launches in a row from a graph; 1 x 1000 x 8192 14.6 in one,
+// 8.7 in 4).
+//
+// One row block: strips of 16 columns, sixteen waves (1 x 4096 x 4096 9.3 against
+// 10.0 with eight, 8192 x 8192 28.0 against 31.2), eight where they are split; and
+// strips of 32 where there are many and the rows are short (1 x 8192 x 1024 6.0
+// against 8.9; 8192 x 8192 29.4). Two row blocks: strips of 32, which halve the
+// loads of x (32 x 8192 x 8192: 37 against 51 with 16). With 48 rows the tiles
+// are level or better (48 x 4096 x 4096 15.7 against 18.0).
 constexpr int64_t FEW_ROWS = 32;
 
-// Its split: a workgroup has 16 columns; a narrow layer's long rows are shared by more.
-struct RowsSplit {
-    int splits, per;
+struct RowsPlan {
+    int wide, waves, ahead; // columns of a strip, waves, k blocks (of 64) a wave loads at once
+    int splits, per;        // workgroups that share a strip, and k blocks for each
 };
-RowsSplit split_rows(int64_t n, int64_t k)
+RowsPlan plan_rows(int64_t m, int64_t n, int64_t k)
 {
-    const int64_t nk = std::max<int64_t>(ceil_div(k, 64), 1), strips = ceil_div(n, 16);
-    const int64_t splits = std::max<int64_t>(1, std::min(UNITS / 2 / strips, nk / 64));
-    RowsSplit s{1, (int)ceil_div(nk, splits)};
-    s.splits = (int)ceil_div(nk, s.per);
-    return s;
+    const int64_t nk = std::max<int64_t>(ceil_div(k, 64), 1);
+    RowsPlan p{32, 8, 2, 1, (int)nk};
+    if (m <= 16 && !(ceil_div(n, 16) > UNITS && nk <= 32))
+        p = ceil_div(n, 16) <= UNITS / 2 ? RowsPlan{16, 8, 4, 1, (int)nk} : RowsPlan{16, 16, 2, 1, (int)nk};
+    const int64_t strips = ceil_div(n, p.wide);
+    const int64_t splits = std::max<int64_t>(1, std::min(UNITS / strips, ceil_div(nk, p.waves * p.ahead)));
+    p.per = (int)ceil_div(nk, splits);
+    p.splits = (int)ceil_div(nk, p.per);
+    return p;
 }
 
-template <int MB, int U> gemm_status run_rows(TileArgs &args, LinearArgs &epi, void *stream)
+template <int MB, int NB, int U, int WAVES>
+gemm_status launch_rows(TileArgs &args, LinearArgs &epi, const RowsPlan &p, void *stream)
 {
-    const RowsSplit s = split_rows(args.n, args.k);
-    args.splits = s.splits;
-    args.split_k = s.per;
-    const gemm_status st = launch_grid(&rows_kernel<MB, U, LinearEpilogue>, ceil_div(args.n, 16), s.splits, 512, stream, args, epi);
-    if (st != GEMM_OK || s.splits == 1)
+    args.splits = p.splits;
+    args.split_k = p.per;
+    const gemm_status st = launch_grid(&rows_kernel<MB, NB, U, WAVES, LinearEpilogue>, ceil_div(args.n, 16 * NB), p.splits, 64 * WAVES,
+                                       stream, args, epi);
+    if (st != GEMM_OK || p.splits == 1)
         return st;
     return launch_grid(&rows_join_kernel<LinearEpilogue>, ceil_div((int64_t)args.m * ((args.n + 7) / 8), 256), 1, 256, stream, args, epi);
+}
+
+gemm_status run_rows(TileArgs &args, LinearArgs &epi, void *stream)
+{
+    const RowsPlan p = plan_rows(args.m, args.n, args.k);
+    if (args.m > 16)
+        return launch_rows<2, 2, 2, 8>(args, epi, p, stream);
+    if (p.wide == 32)
+        return launch_rows<1, 2, 2, 8>(args, epi, p, stream);
+    return p.waves == 16 ? launch_rows<1, 1, 2, 16>(args, epi, p, stream) : launch_rows<1, 1, 4, 8>(args, epi, p, stream);
 }
 
 } // namespace
@@ -44,8 +71,8 @@ int64_t pts_linear_workspace(int64_t m, int64_t n, int64_t k)
     if (!extent(m) || !extent(n) || !extent(k) || m == 0 || n == 0)
         return 0;
     if (m <= FEW_ROWS) {
-        const RowsSplit s = split_rows(n, k);
-        return s.splits == 1 ? 0 : s.splits * m * rows_pitch(n) * (int64_t)sizeof(float);
+        const RowsPlan p = plan_rows(m, n, k);
+        return p.splits == 1 ? 0 : p.splits * m * rows_pitch(n) * (int64_t)sizeof(float);
     }
     return part_bytes(choose_split(m, n, k, 1, false));
 }
@@ -99,10 +126,8 @@ gemm_status pts_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, c
     epi.d_whole = whole_rows(y, ldy, size);
     epi.r_whole = residual != nullptr && whole_rows(residual, ldr, size);
     epi.z_whole = z_out != nullptr && whole_rows(z_out, ldz, 2);
-    if (m <= 16)
-        return run_rows<1, 4>(args, epi, stream);
     if (m <= FEW_ROWS)
-        return run_rows<2, 4>(args, epi, stream);
+        return run_rows(args, epi, stream);
     return run_product<Bf16, ROWS, ROWS, LinearEpilogue>(args, epi, choose_split(m, n, k, 1, false), stream);
 }
 

@@ -61,16 +61,29 @@ def linear(x, w, bias=None, act=None, residual=None):
     return y, z, bound_y, bound_z
 
 
+def slope_bound(dy, z, act):
+    """dz = dy act'(z), and how far its fp32 value may be off: a slope is good to 64 steps of one, and with gelu_tanh to
+    2^-24 of its logistic's argument u, which the logistic (its slope with 2 sqrt(2 / pi) (|z| + 3 0.044715 |z|^3)) carries."""
+    dy = dy.double()
+    if act is None:
+        return dy, torch.zeros_like(dy)
+    z = z.double()
+    steps = torch.full_like(z, 64.0)
+    if act == "gelu_tanh":
+        a = z.abs().clamp(max=16)
+        u = 1.6 * (a + 0.045 * a ** 3)
+        p = torch.sigmoid(-u)
+        steps = steps + 4 * u * (p + p * 1.6 * (a + 0.135 * a ** 3))
+    s = slope(z, act)
+    return dy * s, dy.abs() * steps * HALF[torch.float32] * torch.ones_like(s)
+
+
 def gradients(dy, x, w, z=None, act=None):
     """(dx, dw, dbias, bound of each in fp32): dz's own rounding to bf16, with an activation, is part of the first two."""
-    dy, x, w = dy.double(), x.double(), w.double()
-    dz = dy if act is None else dy * slope(z.double(), act)
+    x, w = x.double(), w.double()
     m, n = dy.shape
     fp32 = HALF[torch.float32]
-    off = torch.zeros_like(dz)
-    if act is not None:     # a slope is good to 64 steps of one, more with gelu_tanh's argument
-        zz = z.double().abs().clamp(max=16)
-        off = dy.abs() * (64 + (4 * (zz + 0.045 * zz ** 3) * slope(z.double(), act).abs() if act == "gelu_tanh" else 0)) * fp32
+    dz, off = slope_bound(dy, z, act)
     mass = dz.abs() + off
     rounded = off if act is None else off + HALF[torch.bfloat16] * mass
     dx, dw = dz @ w, dz.t() @ x

@@ -64,3 +64,55 @@ def test_large_tiles_are_exact_on_integers(pts, m, n, k):
     assert torch.equal(dw, dy.float().t() @ x.float())
     assert torch.equal(dx, (dy.float() @ w.float()).bfloat16())
     assert torch.equal(db, dy.float().sum(0))
+
+
+# Each kernel of few rows: strips of 16 and 32 columns, split and not; their last k blocks whole and ragged.
+@pytest.mark.parametrize("m,n,k", [(1, 4100, 520), (5, 40, 2500), (16, 4200, 64), (16, 1000, 8200), (2, 8200, 1000),
+                                   (1, 4096, 2049), (31, 1000, 4104), (24, 8300, 65), (32, 33, 7), (17, 70, 9000)])
+def test_few_rows_are_exact_on_integers(pts, m, n, k):
+    x, w = padded(m, k, 1, integers=2, pad=float("nan")), padded(n, k, 2, integers=2, pad=float("nan"))
+    assert torch.equal(pts.linear(x, w, out_dtype=F32), x.float() @ w.float().t())
+
+
+def test_zero_sizes(pts):
+    for m, n, k in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (0, 0, 0), (40, 300, 0)):
+        x, w = padded(m, k, 1), padded(n, k, 2)
+        bias = torch.randn(n, device=DEV)
+        y, z = pts.linear(x, w, bias, activation="silu", out_dtype=F32, preactivation=True)
+        want = bias.double().expand(m, n)
+        R.check(y, R.activation(want, "silu"), 32 * R.HALF[F32] * want.abs(), "y")
+        R.check(z, want, torch.zeros_like(want), "z")
+        dy = padded(m, n, 3)
+        dx, dw, db = pts.linear_backward(dy, x, w, z, activation="silu")
+        assert dx.shape == (m, k) and dw.shape == (n, k) and db.shape == (n,)
+        if m == 0 or n == 0:
+            assert not dx.any() and not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("act", R.ACTIVATIONS)
+def test_activation_of_every_value(pts, act):
+    """k = 1 and w = 1: the result is the activation of x, for every finite bf16."""
+    bits = torch.arange(65536, device=DEV, dtype=torch.int32).to(torch.int16)
+    v = bits.view(BF16)
+    v = v[torch.isfinite(v)]
+    x = torch.zeros((v.numel(), 8), device=DEV, dtype=BF16)
+    x[:, 0] = v
+    one = torch.ones((1, 8), device=DEV, dtype=BF16)
+    got = pts.linear(x[:, :1], one[:, :1], activation=act, out_dtype=F32)[:, 0]
+    want, _, bound, _ = R.linear(x[:, :1], one[:, :1], act=act)
+    R.check(got, want[:, 0], bound[:, 0], str(act))
+
+
+@pytest.mark.parametrize("act", R.ACTIVATIONS[1:])
+def test_slope_of_every_value(pts, act):
+    """m = 1 and dy = 1: dbias is the slope at z, dw its rounding, for every finite bf16."""
+    v = torch.arange(65536, device=DEV, dtype=torch.int32).to(torch.int16).view(BF16)
+    v = v[torch.isfinite(v)]
+    z = torch.zeros((1, (v.numel() + 7) // 8 * 8), device=DEV, dtype=BF16)[:, :v.numel()]
+    z[0] = v
+    dy, x, w = torch.ones_like(z), torch.ones((1, 8), device=DEV, dtype=BF16), torch.ones((v.numel(), 8), device=DEV, dtype=BF16)
+    _, dw, db = pts.linear_backward(dy, x, w, z, activation=act, dw_dtype=F32, need_dx=False)
+    want, off = R.slope_bound(dy, z, act)
+    R.check(db, want[0], off[0] + 2 * R.HALF[F32] * want[0].abs(), act)
+    for c in range(8):
+        assert torch.equal(dw[:, c], db.bfloat16().float())
