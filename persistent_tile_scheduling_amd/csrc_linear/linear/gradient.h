@@ -10,22 +10,21 @@ struct SlopeArgs {
     uint16_t *dz;           // null: not written
     float *sums;            // [row blocks][sums_ld], or null
     int64_t ld_dy, ldz, ld_dz, sums_ld;
-    int32_t m, n, act, rows; // rows per workgroup, a multiple of 16
+    int32_t m, n, act, rows; // rows per workgroup
 };
 
 // dz = dy act'(z), rounded to bf16 (the matrix unit's type), and the sums of its
 // columns over the workgroup's rows from the unrounded values. Sixteen threads
-// side by side have 8 columns each, sixteen groups of them every sixteenth row:
-// memory bound, one pass.
-template <int ACT> __device__ __forceinline__ void slope_rows(const SlopeArgs &args, int col, int valid, int row0, int end, float (&sum)[8])
+// side by side have 8 columns each, HIGH groups of them every HIGH-th row: memory
+// bound, one pass.
+template <int ACT, int HIGH> __device__ __forceinline__ void slope_rows(const SlopeArgs &args, int col, int row0, int end, float (&sum)[8])
 {
-    const bool whole = true; // rows start at whole 16 bytes and are read in whole pieces
-    for (int row = row0; row < end; row += 16) {
+    for (int row = row0; row < end; row += HIGH) { // rows start at whole 16 bytes and are read in whole pieces
         float d[8];
-        get8(args.dy + row * args.ld_dy + col, d, 8, whole);
+        get8(args.dy + row * args.ld_dy + col, d, 8, true);
         if constexpr (ACT != ACT_NONE) {
             float z[8];
-            get8(args.z + row * args.ldz + col, z, 8, whole);
+            get8(args.z + row * args.ldz + col, z, 8, true);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 d[i] *= activation_slope<ACT>(z[i]);
@@ -38,15 +37,16 @@ template <int ACT> __device__ __forceinline__ void slope_rows(const SlopeArgs &a
     }
 }
 
-__global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs args)
+template <int HIGH>
+__global__ __launch_bounds__(16 * HIGH) void slope_kernel(const SlopeArgs args)
 {
-    __shared__ __align__(16) float part[16][128 + 4];
+    __shared__ __align__(16) float part[HIGH][128 + 4];
     const int tid = threadIdx.x, x = tid & 15, y = tid >> 4;
-    const int col = blockIdx.x * 128 + x * 8, valid = args.n - col;
+    const int col = blockIdx.x * 128 + x * 8;
     const int row0 = blockIdx.y * args.rows, end = min(args.m, row0 + args.rows);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (valid > 0)
-        with_activation(args.act, [&](auto act) { slope_rows<decltype(act)::value>(args, col, valid, row0 + y, end, sum); });
+    if (col < args.n)
+        with_activation(args.act, [&](auto act) { slope_rows<decltype(act)::value, HIGH>(args, col, row0 + y, end, sum); });
     if (args.sums == nullptr)
         return;
     *(f32x4 *)&part[y][x * 8] = *(f32x4 *)sum;
@@ -55,8 +55,8 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs args)
     const int c = blockIdx.x * 128 + tid;
     if (tid < 128 && c < args.n) {
         float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
+#pragma unroll 16
+        for (int i = 0; i < HIGH; ++i)
             s += part[i][tid];
         args.sums[blockIdx.y * args.sums_ld + c] = s;
     }

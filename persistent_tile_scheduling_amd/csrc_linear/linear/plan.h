@@ -63,26 +63,38 @@ inline Split choose_split(int64_t m, int64_t n, int64_t k, int64_t batch, bool s
 // Bytes of the shared tiles' sums.
 inline int64_t part_bytes(const Split &s) { return s.rest * s.splits * s.edge * s.edge * (int64_t)sizeof(float); }
 
-template <class C, class Epilogue>
-gemm_status launch_tiles(TileArgs &args, typename Epilogue::Args &epi, const Split &s, void *stream)
+template <class C> gemm_status plan_tiles(TileArgs &args, const Split &s, int64_t *grid)
 {
     args.tiles_m = (int32_t)ceil_div(args.m, C::BM);
     args.tiles_n = (int32_t)ceil_div(args.n, C::BN);
     const int64_t tiles = args.symmetric ? (int64_t)args.tiles_m * (args.tiles_m + 1) / 2 : (int64_t)args.tiles_m * args.tiles_n;
-    const int64_t grid = s.whole + s.rest * s.splits;
-    if (grid > INT32_MAX)
+    *grid = s.whole + s.rest * s.splits;
+    if (*grid > INT32_MAX)
         return fail(GEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
     args.tiles = (int32_t)tiles;
     args.whole = (int32_t)s.whole;
     args.rest = (int32_t)s.rest;
     args.splits = s.splits;
     args.split_k = s.per;
-    args.round = (int32_t)std::min<int64_t>(grid, UNITS * (160 * 1024 / C::LDS));
-    const gemm_status st = launch_grid(&tile_kernel<C, Epilogue>, grid, 1, C::THREADS, stream, args, epi);
+    args.round = (int32_t)std::min<int64_t>(*grid, UNITS * (160 * 1024 / C::LDS));
+    return GEMM_OK;
+}
+
+template <class C, class Epilogue>
+gemm_status launch_tiles(TileArgs &args, typename Epilogue::Args &epi, const Split &s, void *stream)
+{
+    int64_t grid;
+    gemm_status st = plan_tiles<C>(args, s, &grid);
+    if (st == GEMM_OK)
+        st = launch_grid(&tile_kernel<C, Epilogue>, grid, 1, C::THREADS, stream, args, epi);
     if (st != GEMM_OK || s.rest == 0)
         return st;
     return launch_grid(&join_kernel<C, Epilogue>, s.rest * (C::BN / 64) * (C::BM / 8) / 4, 1, 256, stream, args, epi);
 }
+
+template <class T, int AF, int BF> using Tiles256 = TileConfig<256, 256, 2, 4, 2, AF, BF, T>;
+template <class T, int AF, int BF> using Tiles128 = TileConfig<128, 128, 2, 2, 2, AF, BF, T>;
+template <class T, int AF, int BF> using Tiles64 = TileConfig<64, 64, 2, 2, 3, AF, BF, T>;
 
 // One product (of a stack of them): the tiles, then the sums of those that were shared.
 template <class T, int AF, int BF, class Epilogue>
@@ -91,10 +103,10 @@ gemm_status run_product(TileArgs &args, typename Epilogue::Args &epi, const Spli
     if (args.m == 0 || args.n == 0 || args.batch == 0)
         return GEMM_OK;
     if (s.edge == 256)
-        return launch_tiles<TileConfig<256, 256, 2, 4, 2, AF, BF, T>, Epilogue>(args, epi, s, stream);
+        return launch_tiles<Tiles256<T, AF, BF>, Epilogue>(args, epi, s, stream);
     if (s.edge == 128)
-        return launch_tiles<TileConfig<128, 128, 2, 2, 2, AF, BF, T>, Epilogue>(args, epi, s, stream);
-    return launch_tiles<TileConfig<64, 64, 2, 2, 3, AF, BF, T>, Epilogue>(args, epi, s, stream);
+        return launch_tiles<Tiles128<T, AF, BF>, Epilogue>(args, epi, s, stream);
+    return launch_tiles<Tiles64<T, AF, BF>, Epilogue>(args, epi, s, stream);
 }
 
 } // namespace pts

@@ -361,16 +361,16 @@ struct Piece {
     }
 };
 
+// Workgroup `block` of `blocks`; smem: C::LDS bytes.
 template <class C, class Epilogue>
-__global__ __launch_bounds__(C::THREADS, 2) void tile_kernel(const TileArgs args, const typename Epilogue::Args epi)
+__device__ __forceinline__ void tile_body(const TileArgs &args, const typename Epilogue::Args &epi, int block, int blocks, uint8_t *smem)
 {
     using OpA = Operand<C::AF, C::BM>;
     using OpB = Operand<C::BF, C::BN>;
-    __shared__ __align__(1024) uint8_t smem[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uniform(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const Tile tile = find_work<C>(args, static_position(blockIdx.x, gridDim.x, args.round));
+    const Tile tile = find_work<C>(args, static_position(block, blocks, args.round));
     const bool loads = wave < C::LOADERS;
     const uint32_t lds = lds_address(smem);
 
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void tile_kernel(const TileArgs args
     const bool tail = args.k % C::BK != 0 && (tile.k0 + tile.nk) * C::BK > args.k;
     const int left = args.k - (tile.k0 + tile.nk - 1) * C::BK;
     const int whole = tile.nk - (tail ? 1 : 0);
-    const int turn = whole > 0 ? (int)(blockIdx.x % NUM_XCD) * 8 % whole : 0;
+    const int turn = whole > 0 ? block % NUM_XCD * 8 % whole : 0;
     auto phys = [&](int kt) {
         if (kt >= whole)
             return tile.k0 + kt;
@@ -552,6 +552,26 @@ __global__ __launch_bounds__(C::THREADS, 2) void tile_kernel(const TileArgs args
                         vn, v, args.symmetric && !tile.diagonal);
         });
     });
+}
+
+template <class C, class Epilogue>
+__global__ __launch_bounds__(C::THREADS, 2) void tile_kernel(const TileArgs args, const typename Epilogue::Args epi)
+{
+    __shared__ __align__(1024) uint8_t smem[C::LDS];
+    tile_body<C, Epilogue>(args, epi, blockIdx.x, gridDim.x, smem);
+}
+
+// Two products that do not wait for each other, one launch: the first `blocks` workgroups are the first's.
+template <class C, class D, class Epilogue>
+__global__ __launch_bounds__(C::THREADS, 2) void tile_pair_kernel(const TileArgs one, const typename Epilogue::Args epi_one, const TileArgs two,
+                                                                  const typename Epilogue::Args epi_two, const int blocks)
+{
+    static_assert(C::THREADS == D::THREADS && C::LDS == D::LDS, "tiles of one shape");
+    __shared__ __align__(1024) uint8_t smem[C::LDS];
+    if ((int)blockIdx.x < blocks)
+        tile_body<C, Epilogue>(one, epi_one, blockIdx.x, blocks, smem);
+    else
+        tile_body<D, Epilogue>(two, epi_two, blockIdx.x - blocks, gridDim.x - blocks, smem);
 }
 
 // The tiles that were split: the sum of their parts, in their order, and the

@@ -8,9 +8,15 @@ namespace {
 
 using namespace pts;
 
+// Up to this many rows one workgroup of 64 rows at a time sums a strip of 128
+// columns, and its sums are the result: a launch less.
+constexpr int64_t ONE_BLOCK = 256;
+
 // Rows of dy per workgroup of the column sums: some 2048 workgroups, and at most 256 row blocks.
 int64_t block_rows(int64_t m, int64_t n)
 {
+    if (m <= ONE_BLOCK)
+        return ONE_BLOCK;
     const int64_t strips = ceil_div(n, 128), blocks = std::max<int64_t>(1, std::min<int64_t>(256, 2048 / strips));
     return ceil_div(ceil_div(m, blocks), 16) * 16;
 }
@@ -27,10 +33,13 @@ Layout layout(int64_t m, int64_t n, int64_t k, int32_t activation)
     l.dx = choose_split(m, k, n, 1, false);
     l.dw = choose_split(n, k, m, 1, false);
     l.sums = activation == PTS_ACTIVATION_NONE ? 0 : round16(m * pitch8(n) * 2);
-    l.part = l.sums + round16(ceil_div(m, block_rows(m, n)) * n * 4);
+    l.part = l.sums + (m <= ONE_BLOCK ? 0 : round16(ceil_div(m, block_rows(m, n)) * n * 4));
     l.all = l.part + std::max(part_bytes(l.dx), part_bytes(l.dw));
     return l;
 }
+
+using TilesX = Tiles64<Bf16, ROWS, COLS>;
+using TilesW = Tiles64<Bf16, COLS, COLS>;
 
 } // namespace
 
@@ -85,50 +94,57 @@ gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, in
             s.ld_dz = ld_dz = pitch8(n);
             dz = s.dz;
         }
-        s.sums = dbias != nullptr ? (float *)(work + l.sums) : nullptr;
+        s.sums = dbias == nullptr ? nullptr : m <= ONE_BLOCK ? dbias : (float *)(work + l.sums);
         s.sums_ld = n;
         s.m = (int32_t)m;
         s.n = (int32_t)n;
         s.rows = (int32_t)block_rows(m, n);
-        if (s.sums != nullptr || s.dz != nullptr)
-            if ((st = launch_grid(&slope_kernel, ceil_div(n, 128), ceil_div(m, s.rows), 256, stream, s)) != GEMM_OK)
+        if (s.sums != nullptr || s.dz != nullptr) {
+            st = m <= ONE_BLOCK ? launch_grid(&slope_kernel<64>, ceil_div(n, 128), 1, 1024, stream, s)
+                                : launch_grid(&slope_kernel<16>, ceil_div(n, 128), ceil_div(m, s.rows), 256, stream, s);
+            if (st != GEMM_OK)
                 return st;
+        }
     }
-    if (dbias != nullptr && n > 0) {
+    if (dbias != nullptr && n > 0 && (m == 0 || m > ONE_BLOCK)) {
         SumArgs s{(const float *)(work + l.sums), dbias, n, (int32_t)n, m > 0 ? (int32_t)ceil_div(m, block_rows(m, n)) : 0};
         if ((st = launch_grid(&sum_kernel, ceil_div(n, 64), 1, 1024, stream, s)) != GEMM_OK)
             return st;
     }
-    TileArgs args{};
-    args.a = dz;
-    args.lda = ld_dz;
-    args.part = (float *)(work + l.part);
-    args.batch = 1;
-    args.n = (int32_t)k;
-    LinearArgs epi{};
-    if (dx != nullptr) {
-        args.b = (const uint16_t *)w;
-        args.ldb = ldw;
-        args.m = (int32_t)m;
-        args.k = (int32_t)n;
-        epi.d = dx;
-        epi.ldd = ld_dx;
-        epi.d_whole = whole_rows(dx, ld_dx, 2);
-        if ((st = run_product<Bf16, ROWS, COLS, PlainEpilogue>(args, epi, l.dx, stream)) != GEMM_OK)
+    TileArgs to_x{}, to_w{};
+    LinearArgs epi_x{}, epi_w{};
+    to_x.a = to_w.a = dz;
+    to_x.lda = to_w.lda = ld_dz;
+    to_x.part = to_w.part = (float *)(work + l.part);
+    to_x.batch = to_w.batch = 1;
+    to_x.n = to_w.n = (int32_t)k;
+    to_x.b = (const uint16_t *)w;
+    to_x.ldb = ldw;
+    to_x.m = (int32_t)m;
+    to_x.k = (int32_t)n;
+    epi_x.d = dx;
+    epi_x.ldd = ld_dx;
+    epi_x.d_whole = whole_rows(dx, ld_dx, 2);
+    to_w.b = (const uint16_t *)x;
+    to_w.ldb = ldx;
+    to_w.m = (int32_t)n;
+    to_w.k = (int32_t)m;
+    epi_w.d = dw;
+    epi_w.ldd = ld_dw;
+    epi_w.d_f32 = dtype_dw == GEMM_DTYPE_F32;
+    epi_w.d_whole = whole_rows(dw, ld_dw, epi_w.d_f32 ? 4 : 2);
+    // small products of unshared tiles in one launch
+    if (dx != nullptr && dw != nullptr && m > 0 && n > 0 && k > 0 && l.dx.edge == 64 && l.dw.edge == 64 && l.dx.rest == 0 && l.dw.rest == 0) {
+        int64_t grid_x, grid_w;
+        if ((st = plan_tiles<TilesX>(to_x, l.dx, &grid_x)) != GEMM_OK || (st = plan_tiles<TilesW>(to_w, l.dw, &grid_w)) != GEMM_OK)
             return st;
+        int blocks = (int)grid_x;
+        return launch_grid(&tile_pair_kernel<TilesX, TilesW, PlainEpilogue>, grid_x + grid_w, 1, TilesX::THREADS, stream, to_x, epi_x,
+                           to_w, epi_w, blocks);
     }
-    if (dw != nullptr) {
-        args.b = (const uint16_t *)x;
-        args.ldb = ldx;
-        args.m = (int32_t)n;
-        args.k = (int32_t)m;
-        epi.d = dw;
-        epi.ldd = ld_dw;
-        epi.d_f32 = dtype_dw == GEMM_DTYPE_F32;
-        epi.d_whole = whole_rows(dw, ld_dw, epi.d_f32 ? 4 : 2);
-        return run_product<Bf16, COLS, COLS, PlainEpilogue>(args, epi, l.dw, stream);
-    }
-    return GEMM_OK;
+    if (dx != nullptr && (st = run_product<Bf16, ROWS, COLS, PlainEpilogue>(to_x, epi_x, l.dx, stream)) != GEMM_OK)
+        return st;
+    return dw == nullptr ? GEMM_OK : run_product<Bf16, COLS, COLS, PlainEpilogue>(to_w, epi_w, l.dw, stream);
 }
 
 } // extern "C"
