@@ -83,7 +83,8 @@ int64_t pts_linear_backward_workspace(int64_t m, int64_t n, int64_t k, int32_t a
  *   X = x / (|x|_F + eps)
  *   `steps` times: X = a X + b (X X^T) X + c (X X^T)^2 X
  * that is p(s) = a s + b s^3 + c s^5 of its singular values. out: bf16, rounded
- * from fp32. The products' operands are fp16 and their sums fp32; X, between the steps, is fp16 and eight bits more.
+ * from fp32. Up to 64 rows or columns all is fp32. Beyond, the products' operands
+ * are fp16 and their sums fp32; X, between the steps, is fp16 and eight bits more.
  *
  * x: row stride ldx >= cols, matrix i at i * x_stride; out likewise (element
  * aligned). 1 <= steps <= 64, eps > 0. The coefficients must keep the singular
@@ -95,7 +96,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
                               int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, double eps,
                               void *out, int64_t ld_out, int64_t out_stride, void *workspace, size_t workspace_bytes,
                               void *stream);
-int64_t pts_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols);
+int64_t pts_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int32_t steps);
 
 #ifdef __cplusplus
 }

@@ -1,5 +1,6 @@
 // Host side of pts_orthogonalize: argument checks and the chain of launches.
 #include "linear/ortho.h"
+#include "linear/ortho_small.h"
 
 #include <cmath>
 
@@ -38,6 +39,24 @@ Layout layout(int64_t count, int64_t rows, int64_t cols)
     return l;
 }
 
+// The same for short sides of up to 64: the squares' sums, the chunks' Gram matrices, the steps' polynomials.
+struct SmallLayout {
+    int64_t parts, polys, all;
+    int32_t blocks, chunks, chunk;
+};
+SmallLayout small_layout(int64_t count, int64_t rows, int64_t cols, int64_t steps)
+{
+    const int64_t lng = std::max(rows, cols);
+    SmallLayout l;
+    l.blocks = (int32_t)std::min<int64_t>(32, ceil_div(rows * ceil_div(cols, 8), 1024));
+    l.chunk = (int32_t)(ceil_div(ceil_div(lng, 64), 32) * 64); // at most 32 chunks: one workgroup adds them up
+    l.chunks = (int32_t)ceil_div(lng, l.chunk);
+    l.parts = round16(count * l.blocks * 8);
+    l.polys = l.parts + count * l.chunks * SMALL_MATRIX * 4;
+    l.all = l.polys + count * steps * SMALL_MATRIX * 4;
+    return l;
+}
+
 bool sizes(int64_t count, int64_t rows, int64_t cols)
 {
     // the workspace's bytes and every product of the extents stay in 64 bits
@@ -73,14 +92,45 @@ double reach(double a, double b, double c, double top)
     return most;
 }
 
+gemm_status run_small(NormArgs &norm, uint8_t *work, void *out, int64_t ldo, int64_t o_batch, int64_t count, int32_t steps, float a,
+                      float b, float c, void *stream)
+{
+    const SmallLayout l = small_layout(count, norm.rows, norm.cols, steps);
+    norm.blocks = l.blocks;
+    SmallArgs args{};
+    args.norm = norm;
+    args.parts = (float *)(work + l.parts);
+    args.polys = (float *)(work + l.polys);
+    args.out = (uint16_t *)out;
+    args.ldo = ldo;
+    args.o_batch = o_batch;
+    args.a = a;
+    args.b = b;
+    args.c = c;
+    args.tall = norm.rows > norm.cols;
+    args.side = std::min(norm.rows, norm.cols);
+    args.lng = std::max(norm.rows, norm.cols);
+    args.chunks = l.chunks;
+    args.chunk = l.chunk;
+    args.steps = steps;
+    gemm_status st;
+    if ((st = launch_grid(&norm_kernel, l.blocks, count, 256, stream, norm)) != GEMM_OK ||
+        (st = launch_grid(&small_gram_kernel, l.chunks, count, 1024, stream, args)) != GEMM_OK ||
+        (st = launch_grid(&small_chain_kernel, count, 1, 1024, stream, args)) != GEMM_OK)
+        return st;
+    return launch_grid(&small_update_kernel, ceil_div(args.lng, 64), count, 256, stream, args);
+}
+
 } // namespace
 
 extern "C" {
 
-int64_t pts_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols)
+int64_t pts_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int32_t steps)
 {
-    if (!sizes(count, rows, cols) || count == 0 || rows == 0 || cols == 0)
+    if (!sizes(count, rows, cols) || count == 0 || rows == 0 || cols == 0 || steps < 1 || steps > 64)
         return 0;
+    if (std::min(rows, cols) <= SMALL)
+        return small_layout(count, rows, cols, steps).all;
     return layout(count, rows, cols).all;
 }
 
@@ -116,33 +166,35 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
     if ((st = check_rows("x", x, ldx, rows * (count > 0), cols, size)) != GEMM_OK ||
         (st = check_rows("out", out, ld_out, rows * (count > 0), cols, 2)) != GEMM_OK)
         return st;
-    if ((st = check_workspace(workspace, workspace_bytes, pts_orthogonalize_workspace(count, rows, cols))) != GEMM_OK)
+    if ((st = check_workspace(workspace, workspace_bytes, pts_orthogonalize_workspace(count, rows, cols, steps))) != GEMM_OK)
         return st;
     if (count == 0 || rows == 0 || cols == 0)
         return GEMM_OK;
 
+    NormArgs norm{};
+    norm.x = x;
+    norm.sums = (double *)workspace;
+    norm.ldx = ldx;
+    norm.x_batch = x_stride;
+    norm.eps = eps;
+    norm.rows = (int32_t)rows;
+    norm.cols = (int32_t)cols;
+    norm.f32 = dtype_x == GEMM_DTYPE_F32;
+    norm.whole = whole_rows(x, ldx, size) && x_stride * size % 16 == 0;
+    if (std::min(rows, cols) <= SMALL)
+        return run_small(norm, (uint8_t *)workspace, out, ld_out, out_stride, count, steps, a, b, c, stream);
     const Layout l = layout(count, rows, cols);
     uint8_t *const work = (uint8_t *)workspace;
     uint16_t *const gram = (uint16_t *)(work + l.gram), *const poly = (uint16_t *)(work + l.poly);
     uint16_t *const half[2] = {(uint16_t *)(work + l.half[0]), (uint16_t *)(work + l.half[1])};
     uint8_t *const rest = work + l.rest;
-    const bool tall = rows > cols, x_whole = whole_rows(x, ldx, size) && x_stride * size % 16 == 0;
+    const bool tall = rows > cols;
     const int64_t side = std::min(rows, cols), lng = std::max(rows, cols);
 
-    NormArgs norm{};
-    norm.x = x;
-    norm.sums = (double *)work;
     norm.scale = (double *)(work + l.scale);
     norm.half = half[0];
-    norm.ldx = ldx;
-    norm.x_batch = x_stride;
     norm.ldh = l.ldx;
     norm.h_batch = rows * l.ldx;
-    norm.eps = eps;
-    norm.rows = (int32_t)rows;
-    norm.cols = (int32_t)cols;
-    norm.f32 = dtype_x == GEMM_DTYPE_F32;
-    norm.whole = x_whole;
     norm.blocks = l.blocks;
     if ((st = launch_grid(&norm_kernel, l.blocks, count, 256, stream, norm)) != GEMM_OK ||
         (st = launch_grid(&start_kernel, ceil_div(rows * ceil_div(cols, 8), 1024), count, 256, stream, norm)) != GEMM_OK)
@@ -203,7 +255,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
             epi.r_type = norm.f32 ? R_F32 : R_BF16;
             epi.ldr = ldx;
             epi.r_batch = x_stride;
-            epi.r_whole = x_whole;
+            epi.r_whole = norm.whole;
         } else {
             epi.beta = a / ORTHO_SX;
             epi.r = now;

@@ -33,7 +33,7 @@ _SIGNATURES = {
     "pts_linear_backward_workspace": (_L, [_L, _L, _L, _I]),
     "pts_linear_backward": (ctypes.c_int, [_P, _L, _P, _L, _I, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _L, _L, _L, _P,
                                            _Z, _P]),
-    "pts_orthogonalize_workspace": (_L, [_L, _L, _L]),
+    "pts_orthogonalize_workspace": (_L, [_L, _L, _L, _I]),
     "pts_orthogonalize": (ctypes.c_int, [_P, _I, _L, _L, _L, _L, _L, _I, _F, _F, _F, _D, _P, _L, _L, _P, _Z, _P]),
 }
 for _name, (_res, _args) in _SIGNATURES.items():
@@ -65,8 +65,8 @@ def pts_linear_backward(*args, stream=None) -> None:
     _call("pts_linear_backward", args, stream)
 
 
-def pts_orthogonalize_workspace(count: int, rows: int, cols: int) -> int:
-    return _lib.pts_orthogonalize_workspace(count, rows, cols)
+def pts_orthogonalize_workspace(count: int, rows: int, cols: int, steps: int) -> int:
+    return _lib.pts_orthogonalize_workspace(count, rows, cols, steps)
 
 
 def pts_orthogonalize(*args, stream=None) -> None:
@@ -249,8 +249,8 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     ``x``: (rows, cols), or (count, rows, cols): a stack of matrices, each by
     itself; bf16 or fp32, rows or columns contiguous. ``out``: bf16, of ``x``'s shape,
     written in place when given, must not share memory with ``x`` (not checked).
-    The products are of fp16 operands, the matrix itself has eight bits more; the
-    coefficients must keep the singular values of [0, 1] below 8 (5 steps of the
+    Up to 64 rows or columns all is fp32; beyond, the products are of fp16 operands
+    and the matrix itself has eight bits more. The coefficients must keep the singular values of [0, 1] below 8 (5 steps of the
     defaults: 1.2).
     """
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or x.dim() not in (2, 3):
@@ -268,10 +268,11 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     ldx, ldo = _pitch("x", x), _pitch("out", out)
     count = x.shape[0] if x.dim() == 3 else 1
     a, b, c = map(float, coefficients)
-    need = _orthogonalize_workspace(count, rows, cols)
+    steps = int(steps)
+    need = _orthogonalize_workspace(count, rows, cols, steps)
     work = _work(need, x.device)
     status = _orthogonalize(x.data_ptr(), _DTYPES[x.dtype], ldx, x.stride(0) if count > 1 else 0, count, rows, cols,
-                            int(steps), a, b, c, float(eps), out.data_ptr(), ldo, out.stride(0) if count > 1 else 0,
+                            steps, a, b, c, float(eps), out.data_ptr(), ldo, out.stride(0) if count > 1 else 0,
                             None if work is None else work.data_ptr(), need, _raw_stream(dev))
     if status:
         _check(status)

@@ -111,6 +111,7 @@ def orthogonalize(x, steps=5, coefficients=QUINTIC, eps=1e-7, rounded=False):
     x = x.double()
     x = x / (x.square().sum((-1, -2), keepdim=True).sqrt() + eps)
     tall = x.shape[-2] > x.shape[-1]
+    rounded = rounded and min(x.shape[-2:]) > 64    # shorter sides are fp32 throughout
 
     def half(v, scale):
         return (v * scale).half().double() / scale if rounded else v

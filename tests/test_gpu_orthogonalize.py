@@ -37,7 +37,8 @@ def check(got, x, **how):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("shape", [(1, 1), (1, 9), (7, 1), (16, 16), (64, 65), (130, 63), (200, 1000), (1025, 257),
-                                   (3, 100, 60), (2, 260, 384)])
+                                   (3, 100, 60), (2, 260, 384), (5, 17, 64), (4, 64, 17), (33, 5000), (5000, 64),
+                                   (2, 9, 20000), (65, 65), (3, 66, 130)])
 def test_orthogonalize(pts, shape, dtype):
     x = matrix(shape, 1, dtype)
     check(pts.orthogonalize(x), x)
