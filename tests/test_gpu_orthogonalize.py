@@ -42,3 +42,95 @@ def check(got, x, **how):
 def test_orthogonalize(pts, shape, dtype):
     x = matrix(shape, 1, dtype)
     check(pts.orthogonalize(x), x)
+
+
+@pytest.mark.parametrize("rank", [1, 5, 30])
+@pytest.mark.parametrize("shape", [(70, 900), (300, 200), (40, 400)])
+def test_low_rank(pts, shape, rank):
+    """Directions that x does not have stay as small as the matrix's sixteen-odd bits leave them."""
+    x = matrix(shape, 3, torch.float32, rank=rank)
+    check(pts.orthogonalize(x), x)
+
+
+@pytest.mark.parametrize("coefficients", [(1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (2.0, -1.5, 0.5), (1.0, 0.0, 0.0)])
+@pytest.mark.parametrize("steps", [1, 2, 9])
+def test_other_steps(pts, steps, coefficients):
+    for shape in ((90, 130), (20, 300)):
+        x = matrix(shape, 4, torch.bfloat16)
+        check(pts.orthogonalize(x, steps, coefficients), x, steps=steps, coefficients=coefficients)
+
+
+@pytest.mark.parametrize("scale", [1e33, 1e-3, 1e-28])
+@pytest.mark.parametrize("shape", [(80, 100), (30, 100)])
+def test_any_scale(pts, shape, scale):
+    """The norm is of 64 bits: a matrix whose squares no float holds comes out the same."""
+    x = matrix(shape, 5, torch.float32) * 1e3
+    eps = 1e-7 * scale
+    check(pts.orthogonalize(x * scale, eps=eps), x * scale, eps=eps)
+
+
+def test_eps_shrinks_small_matrices(pts):
+    for shape in ((80, 100), (30, 100)):
+        x = matrix(shape, 6, torch.float32) * 1e-9
+        check(pts.orthogonalize(x), x)
+
+
+def test_zeros_stay_and_infinities_keep_to_their_matrix(pts):
+    for shape in ((4, 70, 90), (4, 20, 90)):
+        x = matrix(shape, 7, torch.bfloat16)
+        clean = pts.orthogonalize(x)
+        x[0] = 0
+        x[1, 3, 5] = float("inf")
+        x[2, 3, 5] = float("nan")
+        y = pts.orthogonalize(x)
+        assert not y[0].any() and torch.isnan(y[1:3]).all() and torch.equal(y[3], clean[3])
+
+
+@pytest.mark.parametrize("shape", [(70, 200), (200, 70), (30, 200), (3, 90, 101), (3, 20, 101)])
+def test_strides(pts, shape):
+    """Rows that start anywhere, transposes, stacks apart from each other; results in place, nothing else written."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = matrix(shape, 8, dtype)
+        want = pts.orthogonalize(x)
+        wide = torch.full((*shape[:-2], shape[-2] + 3, shape[-1] + 7), float("nan"), device=DEV, dtype=dtype)
+        inside = wide[..., 2:2 + shape[-2], 3:3 + shape[-1]]
+        inside.copy_(x)
+        assert torch.equal(pts.orthogonalize(inside), want)
+        out = torch.full_like(wide, float("nan"), dtype=torch.bfloat16)
+        place = out[..., 1:1 + shape[-2], 5:5 + shape[-1]]
+        assert pts.orthogonalize(inside, out=place) is place and torch.equal(place, want)
+        untouched = torch.ones_like(out, dtype=torch.bool)
+        untouched[..., 1:1 + shape[-2], 5:5 + shape[-1]] = False
+        assert torch.isnan(out[untouched]).all()
+        t = x.transpose(-1, -2).contiguous().transpose(-1, -2)      # the columns are contiguous
+        check(pts.orthogonalize(t), x)
+        turned = torch.full((*shape[:-2], shape[-1], shape[-2]), 0.0, device=DEV, dtype=torch.bfloat16).transpose(-1, -2)
+        assert pts.orthogonalize(t, out=turned) is turned and torch.equal(turned, pts.orthogonalize(t))
+
+
+def test_empty(pts):
+    for shape in ((0, 8), (8, 0), (0, 4, 4), (3, 0, 5)):
+        assert pts.orthogonalize(torch.empty(shape, device=DEV)).shape == shape
+
+
+@pytest.mark.parametrize("shape", [(1100, 1100), (2300, 700), (5, 520, 1000), (600, 6000)])
+def test_larger_tiles(pts, shape):
+    x = matrix(shape, 9, torch.bfloat16)
+    check(pts.orthogonalize(x), x)
+
+
+def test_stack_past_32_bits(pts):
+    """5 GB of matrices, all different: the last ones against the same matrices by themselves and the definition."""
+    count, side = 620, 1450
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((count, side, side), generator=g, device=DEV)
+    y = pts.orthogonalize(x)
+    for i in (0, 409, 410, count - 1):
+        check(y[i], x[i])
+
+
+def test_same_call_same_bits(pts):
+    for shape in ((300, 500), (40, 3000), (2, 500, 300)):
+        x = matrix(shape, 10, torch.bfloat16)
+        first = pts.orthogonalize(x)
+        assert all(torch.equal(first, pts.orthogonalize(x)) for _ in range(3))
