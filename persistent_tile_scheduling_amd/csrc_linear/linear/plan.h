@@ -81,15 +81,21 @@ template <class C> gemm_status plan_tiles(TileArgs &args, const Split &s, int64_
 }
 
 template <class C, class Epilogue>
+gemm_status launch_join(TileArgs &args, typename Epilogue::Args &epi, const Split &s, void *stream)
+{
+    if (s.rest == 0)
+        return GEMM_OK;
+    return launch_grid(&join_kernel<C, Epilogue>, s.rest * (C::BN / 64) * (C::BM / 8) / 4, 1, 256, stream, args, epi);
+}
+
+template <class C, class Epilogue>
 gemm_status launch_tiles(TileArgs &args, typename Epilogue::Args &epi, const Split &s, void *stream)
 {
     int64_t grid;
     gemm_status st = plan_tiles<C>(args, s, &grid);
     if (st == GEMM_OK)
         st = launch_grid(&tile_kernel<C, Epilogue>, grid, 1, C::THREADS, stream, args, epi);
-    if (st != GEMM_OK || s.rest == 0)
-        return st;
-    return launch_grid(&join_kernel<C, Epilogue>, s.rest * (C::BN / 64) * (C::BM / 8) / 4, 1, 256, stream, args, epi);
+    return st != GEMM_OK ? st : launch_join<C, Epilogue>(args, epi, s, stream);
 }
 
 template <class T, int AF, int BF> using Tiles256 = TileConfig<256, 256, 2, 4, 2, AF, BF, T>;

@@ -23,7 +23,7 @@ int64_t block_rows(int64_t m, int64_t n)
 
 // Parts of the workspace, in bytes from its start.
 struct Layout {
-    int64_t sums, part, all; // dz is first
+    int64_t sums, part_x, part_w, all; // dz is first
     Split dx, dw;
 };
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -33,8 +33,9 @@ Layout layout(int64_t m, int64_t n, int64_t k, int32_t activation)
     l.dx = choose_split(m, k, n, 1, false);
     l.dw = choose_split(n, k, m, 1, false);
     l.sums = activation == PTS_ACTIVATION_NONE ? 0 : round16(m * pitch8(n) * 2);
-    l.part = l.sums + (m <= ONE_BLOCK ? 0 : round16(ceil_div(m, block_rows(m, n)) * n * 4));
-    l.all = l.part + std::max(part_bytes(l.dx), part_bytes(l.dw));
+    l.part_x = l.sums + (m <= ONE_BLOCK ? 0 : round16(ceil_div(m, block_rows(m, n)) * n * 4));
+    l.part_w = l.part_x + part_bytes(l.dx);
+    l.all = l.part_w + part_bytes(l.dw);
     return l;
 }
 
@@ -115,7 +116,8 @@ gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, in
     LinearArgs epi_x{}, epi_w{};
     to_x.a = to_w.a = dz;
     to_x.lda = to_w.lda = ld_dz;
-    to_x.part = to_w.part = (float *)(work + l.part);
+    to_x.part = (float *)(work + l.part_x);
+    to_w.part = (float *)(work + l.part_w);
     to_x.batch = to_w.batch = 1;
     to_x.n = to_w.n = (int32_t)k;
     to_x.b = (const uint16_t *)w;
@@ -133,14 +135,17 @@ gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, in
     epi_w.ldd = ld_dw;
     epi_w.d_f32 = dtype_dw == GEMM_DTYPE_F32;
     epi_w.d_whole = whole_rows(dw, ld_dw, epi_w.d_f32 ? 4 : 2);
-    // small products of unshared tiles in one launch
-    if (dx != nullptr && dw != nullptr && m > 0 && n > 0 && k > 0 && l.dx.edge == 64 && l.dw.edge == 64 && l.dx.rest == 0 && l.dw.rest == 0) {
+    // Small products, which do not fill the card by themselves, in one launch (2186 x 48 x 4935 29.3 us with two).
+    if (dx != nullptr && dw != nullptr && m > 0 && n > 0 && k > 0 && l.dx.edge == 64 && l.dw.edge == 64) {
         int64_t grid_x, grid_w;
         if ((st = plan_tiles<TilesX>(to_x, l.dx, &grid_x)) != GEMM_OK || (st = plan_tiles<TilesW>(to_w, l.dw, &grid_w)) != GEMM_OK)
             return st;
         int blocks = (int)grid_x;
-        return launch_grid(&tile_pair_kernel<TilesX, TilesW, PlainEpilogue>, grid_x + grid_w, 1, TilesX::THREADS, stream, to_x, epi_x,
-                           to_w, epi_w, blocks);
+        if ((st = launch_grid(&tile_pair_kernel<TilesX, TilesW, PlainEpilogue>, grid_x + grid_w, 1, TilesX::THREADS, stream, to_x,
+                              epi_x, to_w, epi_w, blocks)) != GEMM_OK ||
+            (st = launch_join<TilesX, PlainEpilogue>(to_x, epi_x, l.dx, stream)) != GEMM_OK)
+            return st;
+        return launch_join<TilesW, PlainEpilogue>(to_w, epi_w, l.dw, stream);
     }
     if (dx != nullptr && (st = run_product<Bf16, ROWS, COLS, PlainEpilogue>(to_x, epi_x, l.dx, stream)) != GEMM_OK)
         return st;

@@ -12,6 +12,7 @@ There is no autograd here: gradients are functions of their own.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -84,9 +85,11 @@ _ACTIVATIONS = {None: PTS_ACTIVATION_NONE, "relu": PTS_ACTIVATION_RELU, "gelu": 
                 "gelu_tanh": PTS_ACTIVATION_GELU_TANH, "silu": PTS_ACTIVATION_SILU}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _empty = torch.empty_strided
-_linear_workspace, _linear = _lib.pts_linear_workspace, _lib.pts_linear
-_backward_workspace, _backward = _lib.pts_linear_backward_workspace, _lib.pts_linear_backward
-_orthogonalize_workspace, _orthogonalize = _lib.pts_orthogonalize_workspace, _lib.pts_orthogonalize
+_linear, _backward, _orthogonalize = _lib.pts_linear, _lib.pts_linear_backward, _lib.pts_orthogonalize
+# Sizes alone decide a workspace's bytes: the call into the library is made once for each.
+_linear_workspace = functools.lru_cache(1024)(_lib.pts_linear_workspace)
+_backward_workspace = functools.lru_cache(1024)(_lib.pts_linear_backward_workspace)
+_orthogonalize_workspace = functools.lru_cache(1024)(_lib.pts_orthogonalize_workspace)
 
 
 def _operand(name, t) -> int:
@@ -116,11 +119,10 @@ def _pitch(name, t) -> int:
 
 
 def _padded(m, n, dtype, device):
-    """An (m, n) result whose rows start at whole 16 bytes, and its row stride."""
+    """An (m, n) result whose rows start at whole 16 bytes, and its row stride. What the last row lacks to a whole piece,
+    up to the next 16 bytes, belongs to the allocation, whose size is a multiple of more."""
     ld = (n + 7) // 8 * 8
-    if ld == n:
-        return _empty((m, n), (n, 1), dtype=dtype, device=device), n
-    return torch.empty((m, ld), dtype=dtype, device=device)[:, :n], ld
+    return _empty((m, n), (ld, 1), dtype=dtype, device=device), ld
 
 
 def _work(need, device):
