@@ -10,7 +10,9 @@
 namespace pts {
 
 inline bool extent(int64_t v) { return v >= 0 && v < MAX_EXTENT; }
-inline int64_t pitch8(int64_t n) { return (n + 7) / 8 * 8; }
+// Row stride of the library's own 16-bit matrices: rows start at whole cache lines, since a k tile of a row that starts
+// inside one takes two (dx of 5000 x 7000 x 3000: 204 us, 178 with aligned rows of dz).
+inline int64_t own_pitch(int64_t n) { return (n + 63) / 64 * 64; }
 
 // A bf16 operand that the matrix unit reads: rows x width.
 inline gemm_status check_operand(const char *name, const void *p, int64_t ld, int64_t rows, int64_t width)

@@ -52,14 +52,15 @@ __device__ __forceinline__ float small_x(const SmallArgs &args, int batch, int i
     return (float)((double)v * scale);
 }
 
-// acc += (rows of p) . (rows of q), 16 k at a time: lane l has of row l % 16 the k 4 (l / 16) .. + 3, and gets of the
+// acc += (rows of p) . (rows of q) over `blocks` times 16 k: lane l has of row l % 16 the k 4 (l / 16) .. + 3, and gets of the
 // result row 4 (l / 16) .. + 3 of p against row l % 16 of q.
-template <int K>
-__device__ __forceinline__ f32x4 small_product(const float *p, const float *q, int lane, f32x4 acc)
+__device__ __forceinline__ f32x4 small_product(const float *p, const float *q, int blocks, int lane, f32x4 acc)
 {
     const int at = (lane & 15) * SMALL_PITCH + (lane >> 4) * 4;
 #pragma unroll
-    for (int k = 0; k < K; k += 16) {
+    for (int k = 0; k < SMALL; k += 16) {
+        if (k >= blocks * 16)
+            break;
         const f32x4 x = *(const f32x4 *)(p + at + k), y = *(const f32x4 *)(q + at + k);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(1024) void small_gram_kernel(const SmallArgs args)
             x[i * SMALL_PITCH + j] = v[u];
         }
         barrier_lds();
-        acc = small_product<64>(x + r * 16 * SMALL_PITCH, x + c * 16 * SMALL_PITCH, lane, acc);
+        acc = small_product(x + r * 16 * SMALL_PITCH, x + c * 16 * SMALL_PITCH, 4, lane, acc);
     }
     float *const part = args.parts + ((int64_t)batch * args.chunks + blockIdx.x) * SMALL_MATRIX;
 #pragma unroll
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(1024) void small_chain_kernel(const SmallArgs args)
 {
     __shared__ __align__(16) float A[SMALL * SMALL_PITCH], Q[SMALL * SMALL_PITCH], T[SMALL * SMALL_PITCH];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int batch = blockIdx.x, r = wave >> 2, c = wave & 3;
+    const int batch = blockIdx.x, r = wave >> 2, c = wave & 3, blocks = (args.side + 15) / 16;
     const int col = c * 16 + (lane & 15), row = r * 16 + (lane >> 4) * 4;
     const float *const part = args.parts + (int64_t)batch * args.chunks * SMALL_MATRIX;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(1024) void small_chain_kernel(const SmallArgs args)
         *(f32x4 *)(T + at) = zero;
     }
     float *poly = args.polys + (int64_t)batch * args.steps * SMALL_MATRIX + row * SMALL + col;
-    auto product = [&](const float *p, const float *q) { return small_product<64>(p + r * 16 * SMALL_PITCH, q + c * 16 * SMALL_PITCH, lane, zero); };
+    auto product = [&](const float *p, const float *q) { return small_product(p + r * 16 * SMALL_PITCH, q + c * 16 * SMALL_PITCH, blocks, lane, zero); };
     barrier_lds();
     for (int s = 0; s < args.steps; ++s, poly += SMALL_MATRIX) {
         if (used) {
@@ -159,19 +160,31 @@ __global__ __launch_bounds__(256) void small_update_kernel(const SmallArgs args)
     const int batch = blockIdx.y, blocks = (args.side + 15) / 16;
     const int64_t j0 = (int64_t)blockIdx.x * 64;
     const double scale = small_scale(args, batch);
-#pragma unroll 4
-    for (int at = tid; at < SMALL * 64; at += 256) {
-        const int i = args.tall ? at & 63 : at >> 6, j = args.tall ? at >> 6 : at & 63;
-        x[j * SMALL_PITCH + i] = small_x(args, batch, i, j0 + j, scale);
+    constexpr int EACH = SMALL * 64 / 256;
+    float v[EACH];
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+        const int at = u * 256 + tid, i = args.tall ? at & 63 : at >> 6, j = args.tall ? at >> 6 : at & 63;
+        v[u] = small_x(args, batch, i, j0 + j, scale);
+    }
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+        const int at = u * 256 + tid, i = args.tall ? at & 63 : at >> 6, j = args.tall ? at >> 6 : at & 63;
+        x[j * SMALL_PITCH + i] = v[u];
     }
     float *const mine = x + wave * 16 * SMALL_PITCH;
-    for (int s = 0; s < args.steps; ++s) {
-        const float *const from = args.polys + ((int64_t)batch * args.steps + s) * SMALL_MATRIX;
-        f32x4 p[4];
+    // a step's polynomial is on its way while the step before it runs
+    f32x4 p[4];
+    const float *from = args.polys + (int64_t)batch * args.steps * SMALL_MATRIX + tid * 4;
+    auto fetch = [&] {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (u * 16 < args.side) // rows past the side are not written
-                p[u] = *(const f32x4 *)(from + u * 1024 + tid * 4);
+                p[u] = *(const f32x4 *)(from + u * 1024);
+        from += SMALL_MATRIX;
+    };
+    fetch();
+    for (int s = 0; s < args.steps; ++s) {
         barrier_lds(); // the step before has been read
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -179,6 +192,8 @@ __global__ __launch_bounds__(256) void small_update_kernel(const SmallArgs args)
                 const int i = u * 16 + tid / 16, k = tid % 16 * 4;
                 *(f32x4 *)(poly + i * SMALL_PITCH + k) = k / 16 < blocks ? p[u] : f32x4{0.f, 0.f, 0.f, 0.f};
             }
+        if (s + 1 < args.steps)
+            fetch();
         barrier_lds();
         f32x4 acc[4];
         const int at = (lane & 15) * SMALL_PITCH + (lane >> 4) * 4; // of vector lane % 16, four elements of each block
@@ -186,7 +201,7 @@ __global__ __launch_bounds__(256) void small_update_kernel(const SmallArgs args)
         for (int i = 0; i < 4; ++i)
             if (i < blocks) {
                 const f32x4 v = *(const f32x4 *)(mine + at + i * 16);
-                acc[i] = small_product<64>(poly + i * 16 * SMALL_PITCH, mine, lane, f32x4{args.a * v[0], args.a * v[1], args.a * v[2], args.a * v[3]});
+                acc[i] = small_product(poly + i * 16 * SMALL_PITCH, mine, blocks, lane, f32x4{args.a * v[0], args.a * v[1], args.a * v[2], args.a * v[3]});
             }
         wave_lds_exchange();
 #pragma unroll

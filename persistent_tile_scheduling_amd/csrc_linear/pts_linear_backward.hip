@@ -32,7 +32,7 @@ Layout layout(int64_t m, int64_t n, int64_t k, int32_t activation)
     Layout l;
     l.dx = choose_split(m, k, n, 1, false);
     l.dw = choose_split(n, k, m, 1, false);
-    l.sums = activation == PTS_ACTIVATION_NONE ? 0 : round16(m * pitch8(n) * 2);
+    l.sums = activation == PTS_ACTIVATION_NONE ? 0 : round16(m * own_pitch(n) * 2);
     l.part_x = l.sums + (m <= ONE_BLOCK ? 0 : round16(ceil_div(m, block_rows(m, n)) * n * 4));
     l.part_w = l.part_x + part_bytes(l.dx);
     l.all = l.part_w + part_bytes(l.dw);
@@ -92,7 +92,7 @@ gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, in
         s.act = activation;
         if (act && (dx != nullptr || dw != nullptr)) {
             s.dz = (uint16_t *)work;
-            s.ld_dz = ld_dz = pitch8(n);
+            s.ld_dz = ld_dz = own_pitch(n);
             dz = s.dz;
         }
         s.sums = dbias == nullptr ? nullptr : m <= ONE_BLOCK ? dbias : (float *)(work + l.sums);

@@ -22,8 +22,8 @@ Layout layout(int64_t count, int64_t rows, int64_t cols)
 {
     const int64_t side = std::min(rows, cols), lng = std::max(rows, cols);
     Layout l;
-    l.ldx = pitch8(cols);
-    l.lds = pitch8(side);
+    l.ldx = own_pitch(cols);
+    l.lds = own_pitch(side);
     l.gram_split = choose_split(side, side, lng, count, true);
     l.square_split = choose_split(side, side, side, count, true);
     l.update_split = choose_split(rows, cols, side, count, false);
