@@ -13,7 +13,7 @@
  * Results are deterministic: no sum's order depends on timing.
  *
  * bf16 operands (x, w, dy, z) start 16-byte aligned and have row strides that are
- * multiples of 8 elements and below 2^23; rows are read in whole 16-byte pieces
+ * multiples of 8 elements and below 2^22; rows are read in whole 16-byte pieces
  * (up to their width rounded up to 8), what lies past their width does not count.
  * Extents are below 2^31 - 1024. A problem that takes 2^32 threads or more in one
  * launch is GEMM_ERR_UNSUPPORTED.
@@ -87,10 +87,12 @@ int64_t pts_linear_backward_workspace(int64_t m, int64_t n, int64_t k, int32_t a
  * are fp16 and their sums fp32; X, between the steps, is fp16 and eight bits more.
  *
  * x: row stride ldx >= cols, matrix i at i * x_stride; out likewise (element
- * aligned). 1 <= steps <= 64, eps > 0. The coefficients must keep the singular
- * values, which start within [0, 1], in fp16's reach: GEMM_ERR_INVALID_VALUE if
- * |p| can come above 8 or |b s^2 + c s^4| above 128 on the way. A matrix with an
- * infinity or a NaN comes out NaN; a matrix of zeros stays zero.
+ * aligned; its matrices must not overlap). cols and the smaller of rows and cols
+ * are at most 2^22 - 64, count 65535. 1 <= steps <= 64, eps > 0. The coefficients
+ * must keep the singular values, which start within [0, 1], in fp16's reach:
+ * GEMM_ERR_INVALID_VALUE if |p| can come above 8 or |b s^2 + c s^4| above 128 on
+ * the way. A matrix with an infinity or a NaN comes out NaN; a matrix of zeros
+ * stays zero.
  */
 gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64_t x_stride, int64_t count,
                               int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, double eps,

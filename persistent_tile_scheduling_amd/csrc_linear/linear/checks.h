@@ -9,6 +9,7 @@
 
 namespace pts {
 
+constexpr int64_t MAX_PITCH = 1 << 22; // elements: 256 rows of them are within 2^31 bytes
 inline bool extent(int64_t v) { return v >= 0 && v < MAX_EXTENT; }
 // Row stride of the library's own 16-bit matrices: rows start at whole cache lines, since a k tile of a row that starts
 // inside one takes two (dx of 5000 x 7000 x 3000: 204 us, 178 with aligned rows of dz).
@@ -22,7 +23,7 @@ inline gemm_status check_operand(const char *name, const void *p, int64_t ld, in
                     (long long)width);
     if (ld % 8 != 0)
         return fail(GEMM_ERR_INVALID_VALUE, "%s: leading dimension %lld is not a multiple of 8 elements", name, (long long)ld);
-    if (ld >= 1 << 23)
+    if (ld >= MAX_PITCH)
         return fail(GEMM_ERR_UNSUPPORTED, "%s: leading dimension %lld: a tile's offsets must fit in 32-bit", name, (long long)ld);
     if (rows > 0 && width > 0 && p == nullptr)
         return fail(GEMM_ERR_INVALID_VALUE, "%s: NULL pointer", name);

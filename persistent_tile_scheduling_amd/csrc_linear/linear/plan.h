@@ -63,14 +63,24 @@ inline Split choose_split(int64_t m, int64_t n, int64_t k, int64_t batch, bool s
 // Bytes of the shared tiles' sums.
 inline int64_t part_bytes(const Split &s) { return s.rest * s.splits * s.edge * s.edge * (int64_t)sizeof(float); }
 
+// Whether its launches keep within HIP's 2^32 - 1 threads.
+inline gemm_status check_launches(const Split &s)
+{
+    const int64_t grid = s.whole + s.rest * s.splits;
+    if (grid > (int64_t)UINT32_MAX / (s.edge == 256 ? 512 : 256))
+        return fail(GEMM_ERR_UNSUPPORTED, "%lld workgroups: too large a problem for one launch", (long long)grid);
+    return GEMM_OK;
+}
+
 template <class C> gemm_status plan_tiles(TileArgs &args, const Split &s, int64_t *grid)
 {
     args.tiles_m = (int32_t)ceil_div(args.m, C::BM);
     args.tiles_n = (int32_t)ceil_div(args.n, C::BN);
     const int64_t tiles = args.symmetric ? (int64_t)args.tiles_m * (args.tiles_m + 1) / 2 : (int64_t)args.tiles_m * args.tiles_n;
     *grid = s.whole + s.rest * s.splits;
-    if (*grid > INT32_MAX)
-        return fail(GEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+    const gemm_status st = check_launches(s);
+    if (st != GEMM_OK)
+        return st;
     args.tiles = (int32_t)tiles;
     args.whole = (int32_t)s.whole;
     args.rest = (int32_t)s.rest;

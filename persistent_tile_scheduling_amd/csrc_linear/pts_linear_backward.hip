@@ -80,6 +80,10 @@ gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, in
         return GEMM_OK;
 
     const Layout l = layout(std::max<int64_t>(m, 1), std::max<int64_t>(n, 1), k, activation);
+    if ((dx != nullptr && (st = check_launches(l.dx)) != GEMM_OK) || (dw != nullptr && (st = check_launches(l.dw)) != GEMM_OK))
+        return st;
+    if (ceil_div(n, 128) * ceil_div(std::max<int64_t>(m, 1), block_rows(m, std::max<int64_t>(n, 1))) > (int64_t)UINT32_MAX / 1024)
+        return fail(GEMM_ERR_UNSUPPORTED, "n = %lld: too large a problem for one launch", (long long)n);
     uint8_t *const work = (uint8_t *)workspace;
     const uint16_t *dz = (const uint16_t *)dy;
     int64_t ld_dz = ld_dy;

@@ -145,8 +145,8 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         return fail(GEMM_ERR_INVALID_VALUE, "count, rows and cols must be in [0, 2^31 - 1024), count * rows * cols at most 2^48");
     if (count > 65535)
         return fail(GEMM_ERR_UNSUPPORTED, "%lld matrices; at most 65535", (long long)count);
-    if (std::min(rows, cols) >= 1 << 23 || cols >= (1 << 23) - 8)
-        return fail(GEMM_ERR_UNSUPPORTED, "a tile's offsets must fit in 32-bit: fewer than 2^23 - 8 columns");
+    if (cols > MAX_PITCH - 64 || std::min(rows, cols) > MAX_PITCH - 64)
+        return fail(GEMM_ERR_UNSUPPORTED, "a tile's offsets must fit in 32-bit: at most 2^22 - 64 columns");
     if (steps < 1 || steps > 64)
         return fail(GEMM_ERR_INVALID_VALUE, "steps must be in [1, 64], not %d", steps);
     if (!(eps > 0.0))
@@ -166,10 +166,17 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
     if ((st = check_rows("x", x, ldx, rows * (count > 0), cols, size)) != GEMM_OK ||
         (st = check_rows("out", out, ld_out, rows * (count > 0), cols, 2)) != GEMM_OK)
         return st;
+    if (count > 1 && rows > 0 && cols > 0 && out_stride < (rows - 1) * ld_out + cols &&
+        (out_stride < cols || ld_out < (count - 1) * out_stride + cols))
+        return fail(GEMM_ERR_INVALID_VALUE, "out's matrices overlap (stride %lld)", (long long)out_stride);
     if ((st = check_workspace(workspace, workspace_bytes, pts_orthogonalize_workspace(count, rows, cols, steps))) != GEMM_OK)
         return st;
     if (count == 0 || rows == 0 || cols == 0)
         return GEMM_OK;
+    const bool small = std::min(rows, cols) <= SMALL;
+    if (small && ceil_div(std::max(rows, cols), 64) * count > (int64_t)UINT32_MAX / 256)
+        return fail(GEMM_ERR_UNSUPPORTED, "%lld x %lld x %lld: too large a problem for one launch", (long long)count, (long long)rows,
+                    (long long)cols);
 
     NormArgs norm{};
     norm.x = x;
@@ -181,9 +188,12 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
     norm.cols = (int32_t)cols;
     norm.f32 = dtype_x == GEMM_DTYPE_F32;
     norm.whole = whole_rows(x, ldx, size) && x_stride * size % 16 == 0;
-    if (std::min(rows, cols) <= SMALL)
+    if (small)
         return run_small(norm, (uint8_t *)workspace, out, ld_out, out_stride, count, steps, a, b, c, stream);
     const Layout l = layout(count, rows, cols);
+    for (const Split *s : {&l.gram_split, &l.square_split, &l.update_split})
+        if ((st = check_launches(*s)) != GEMM_OK)
+            return st;
     uint8_t *const work = (uint8_t *)workspace;
     uint16_t *const gram = (uint16_t *)(work + l.gram), *const poly = (uint16_t *)(work + l.poly);
     uint16_t *const half[2] = {(uint16_t *)(work + l.half[0]), (uint16_t *)(work + l.half[1])};
@@ -197,7 +207,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
     norm.h_batch = rows * l.ldx;
     norm.blocks = l.blocks;
     if ((st = launch_grid(&norm_kernel, l.blocks, count, 256, stream, norm)) != GEMM_OK ||
-        (st = launch_grid(&start_kernel, ceil_div(rows * ceil_div(cols, 8), 1024), count, 256, stream, norm)) != GEMM_OK)
+        (st = launch_grid(&start_kernel, std::min<int64_t>(ceil_div(rows * ceil_div(cols, 8), 1024), std::max<int64_t>(1, 65536 / count)), count, 256, stream, norm)) != GEMM_OK)
         return st;
 
     for (int i = 0; i < steps; ++i) {

@@ -51,7 +51,7 @@ LINEAR = dict(x=P, ldx=64, w=P, ldw=64, bias=None, dtype_bias=0, act=0, residual
     (dict(dtype=2), 2, "fp32 or bf16"), (dict(bias=P, dtype_bias=3), 2, "fp32 or bf16"), (dict(act=5), 1, "activation"),
     (dict(act=-1), 1, "activation"), (dict(m=-1), 1, "m, n and k"), (dict(n=2 ** 31), 1, "m, n and k"),
     (dict(k=2 ** 31 - 1024, ldx=2 ** 31, ldw=2 ** 31), 1, "m, n and k"), (dict(ldx=56), 1, "x: leading"),
-    (dict(ldw=60, k=60), 1, "w: leading"), (dict(ldx=68), 1, "multiple of 8"), (dict(ldw=1 << 23), 2, "32-bit"),
+    (dict(ldw=60, k=60), 1, "w: leading"), (dict(ldx=68), 1, "multiple of 8"), (dict(ldw=1 << 22), 2, "32-bit"),
     (dict(x=P + 8), 1, "x must be 16-byte"), (dict(w=P + 2), 1, "w must be 16-byte"), (dict(x=None), 1, "x: NULL"),
     (dict(y=None), 1, "y: NULL"), (dict(ldy=39), 1, "y: leading"), (dict(ldy=2 ** 62), 1, "y: leading"),
     (dict(y=P + 1), 1, "y must be element"), (dict(dtype=1, y=P + 2), 1, "y must be element"),
@@ -74,7 +74,7 @@ BACK = dict(dy=P, ld_dy=40, z=P, ldz=40, act=4, x=P, ldx=64, w=P, ldw=64, dx=P, 
     (dict(ld_dy=36), 1, "dy: leading"), (dict(ld_dy=44), 1, "dy: leading"), (dict(z=None), 1, "z: NULL"),
     (dict(z=P + 4), 1, "z must be 16-byte"), (dict(ldx=60), 1, "x: leading"), (dict(w=None), 1, "w: NULL"),
     (dict(x=None), 1, "x: NULL"), (dict(ld_dx=63), 1, "dx: leading"), (dict(ld_dw=63), 1, "dw: leading"),
-    (dict(dw=P + 2, dtype=1), 1, "dw must be element"), (dict(db=P + 2), 1, "dbias"), (dict(bytes=0), 1, "workspace"),
+    (dict(dw=P + 2, dtype=1), 1, "dw must be element"), (dict(m=2 ** 31 - 2048, k=300, ldx=304, ldw=304, ld_dx=304, ld_dw=304), 2, "too large"), (dict(db=P + 2), 1, "dbias"), (dict(bytes=0), 1, "workspace"),
 ])
 def test_backward_refusals(pts, change, status, fragment):
     _refused(pts, lambda: pts.pts_linear_backward(*{**BACK, **change}.values(), stream=0), status, fragment)
@@ -87,11 +87,13 @@ ORTHO = dict(x=P, dtype=0, ldx=64, xs=0, count=1, rows=40, cols=64, steps=5, a=3
 @pytest.mark.parametrize("change,status,fragment", [
     (dict(dtype=2), 2, "fp32 or bf16"), (dict(count=-1), 1, "count"), (dict(rows=2 ** 31 - 1024), 1, "count"),
     (dict(rows=2 ** 30, cols=2 ** 22, ldx=2 ** 22, ldo=2 ** 22), 1, "2^48"), (dict(count=65536), 2, "65535"),
-    (dict(cols=1 << 23, ldx=1 << 23, ldo=1 << 23), 2, "32-bit"), (dict(steps=0), 1, "steps"), (dict(steps=65), 1, "steps"),
+    (dict(cols=(1 << 22) - 63, ldx=1 << 22, ldo=1 << 22), 2, "32-bit"), (dict(steps=0), 1, "steps"), (dict(steps=65), 1, "steps"),
     (dict(eps=0.0), 1, "eps"), (dict(eps=float("nan")), 1, "eps"), (dict(a=9.0), 1, "fp16's reach"),
     (dict(a=2.0, b=2.0, c=2.0), 1, "fp16's reach"), (dict(a=float("nan")), 1, "fp16's reach"),
     (dict(a=1.0, b=-200.0, c=200.0), 1, "fp16's reach"), (dict(ldx=63), 1, "x: leading"), (dict(ldo=63), 1, "out: leading"),
     (dict(x=None), 1, "x: NULL"), (dict(out=P + 1), 1, "out must be"), (dict(dtype=1, x=P + 2), 1, "x must be"),
+    (dict(count=2, os=63), 1, "overlap"), (dict(count=2, ldo=100, os=64), 1, "overlap"),
+    (dict(count=65535, rows=64, cols=1 << 15, ldx=1 << 15, ldo=1 << 15, os=1 << 21), 2, "too large"),
     (dict(xs=-1), 1, "strides"), (dict(count=2, os=2 ** 62), 1, "strides"), (dict(bytes=64), 1, "workspace"),
 ])
 def test_orthogonalize_refusals(pts, change, status, fragment):
