@@ -14,7 +14,8 @@ constexpr int64_t UNITS = 256; // compute units of the card: the choice, and wit
 constexpr int64_t MAX_EXTENT = INT32_MAX - 1024; // extents are rounded up to whole tiles in 32 bits
 
 struct Split {
-    int edge;            // tiles are edge x edge
+    int edge;            // tiles are edge x edge,
+    bool wide;           //   128 x 128 ones by eight waves with a ring of four stages, one to a compute unit
     int splits, per;     // workgroups that share a tile's contraction, and k tiles (of 64) for each:
     int64_t whole, rest; //   so many tiles are not shared, so many are
 };
@@ -24,11 +25,15 @@ struct Split {
 // with 256 and 512 tiles of 512, 4096 and 8192 k; the three ways the operands can
 // lie differ by 10%). So 256 x 256 tiles run at 1470 to 1590 TFLOP/s, 128 x 128 at
 // 1190 to 1260 (840 to 1060 alone), 64 x 64 at 650 to 790 (470 to 530 alone).
+// Where a unit has one 128 x 128 tile only, eight waves and a ring of four stages
+// hide more of the loads' latency than four waves and two (2048^3 21.0 us against
+// 25.8, 4096 x 1024 x 4096 36.3 against 44.5; with two tiles to a unit, 4096 x 2048
+// x 8192, 132 against 118).
 struct TileCost {
     int edge, resident;
     double alone, paired, fixed;
 };
-constexpr TileCost TILE_COSTS[] = {{256, 1, 1.40, 1.40, 7.0}, {128, 2, 0.54, 0.87, 5.0}, {64, 2, 0.27, 0.38, 3.0}};
+constexpr TileCost TILE_COSTS[] = {{256, 1, 1.40, 1.40, 7.0}, {128, 2, 0.54, 0.87, 5.0}, {128, 1, 0.46, 0.46, 5.0}, {64, 2, 0.27, 0.38, 3.0}};
 constexpr double JOIN_US = 4.0, JOIN_BYTES_PER_US = 2.5e6; // a launch; a part written and read again
 
 // The tiles, and how the last round of them, which seldom fills the card, is
@@ -53,7 +58,8 @@ inline Split choose_split(int64_t m, int64_t n, int64_t k, int64_t batch, bool s
                 us += JOIN_US + (double)(rest * used * c.edge * c.edge * 4) / JOIN_BYTES_PER_US;
             if (us < least) {
                 least = us;
-                best = used > 1 ? Split{c.edge, (int)used, (int)per, whole, rest} : Split{c.edge, 1, (int)nk, tiles, 0};
+                const bool wide = c.edge == 128 && c.resident == 1;
+                best = used > 1 ? Split{c.edge, wide, (int)used, (int)per, whole, rest} : Split{c.edge, wide, 1, (int)nk, tiles, 0};
             }
         }
     }
@@ -67,7 +73,7 @@ inline int64_t part_bytes(const Split &s) { return s.rest * s.splits * s.edge * 
 inline gemm_status check_launches(const Split &s)
 {
     const int64_t grid = s.whole + s.rest * s.splits;
-    if (grid > (int64_t)UINT32_MAX / (s.edge == 256 ? 512 : 256))
+    if (grid > (int64_t)UINT32_MAX / (s.edge == 256 || s.wide ? 512 : 256))
         return fail(GEMM_ERR_UNSUPPORTED, "%lld workgroups: too large a problem for one launch", (long long)grid);
     return GEMM_OK;
 }
@@ -110,6 +116,7 @@ gemm_status launch_tiles(TileArgs &args, typename Epilogue::Args &epi, const Spl
 
 template <class T, int AF, int BF> using Tiles256 = TileConfig<256, 256, 2, 4, 2, AF, BF, T>;
 template <class T, int AF, int BF> using Tiles128 = TileConfig<128, 128, 2, 2, 2, AF, BF, T>;
+template <class T, int AF, int BF> using TilesWide128 = TileConfig<128, 128, 2, 4, 4, AF, BF, T>;
 template <class T, int AF, int BF> using Tiles64 = TileConfig<64, 64, 2, 2, 3, AF, BF, T>;
 
 // One product (of a stack of them): the tiles, then the sums of those that were shared.
@@ -120,6 +127,8 @@ gemm_status run_product(TileArgs &args, typename Epilogue::Args &epi, const Spli
         return GEMM_OK;
     if (s.edge == 256)
         return launch_tiles<Tiles256<T, AF, BF>, Epilogue>(args, epi, s, stream);
+    if (s.wide)
+        return launch_tiles<TilesWide128<T, AF, BF>, Epilogue>(args, epi, s, stream);
     if (s.edge == 128)
         return launch_tiles<Tiles128<T, AF, BF>, Epilogue>(args, epi, s, stream);
     return launch_tiles<Tiles64<T, AF, BF>, Epilogue>(args, epi, s, stream);
