@@ -1,16 +1,14 @@
 // The activations of a linear layer and their slopes, in fp32.
 //
-// They stand in a product's epilogue, where eight waves put 65536 values through
-// them with nothing else to do: 5 to 20 us a tile by their number of instructions.
-// So an activation takes the hardware's exponential and reciprocal as they are: it
-// is good to 16 steps of 2^-24 of its value and as many more as its exponential's
-// argument is large (the rounding of that argument): 2^-20 of the value for |z| < 5.
-// What lies below 2^-119, and silu and gelu_tanh left of an argument of -88, is 0.
-// (8192^3 with gelu_tanh, bias and residual: 842 us with corrected ones.)
-//
-// A slope, in a pass bound by memory, takes corrected ones: to a few steps of its
-// value and, near its own zero, of one; only gelu_tanh's adds the rounding of its
-// logistic's argument u, 2^-24 |u|.
+// An activation stands in a product's epilogue, where eight waves put 65536 values
+// through it with nothing else to do, its slope in a pass that gelu's would bound
+// by its instructions (5000 x 7000: 53 us with corrected exponentials and
+// reciprocals, 48 without). So both take the hardware's as they are. An
+// activation is good to 16 steps of 2^-24 of its value and, from the rounding of
+// its exponential's argument, 3 |argument| more: 2^-20 of the value for |z| < 5. A
+// slope is good to 64 steps of one; gelu_tanh's adds the rounding of its logistic's
+// argument u, 2^-24 |u|, times that logistic's slope. What lies below 2^-119, and
+// silu and gelu_tanh left of an argument of -88, is 0.
 //
 // gelu is z Phi(z). With a = |z|, Phi(-a) = exp(-a^2 / 2) G(a), where G(a) =
 // erfcx(a / sqrt 2) / 2 falls smoothly from 1/2 like 1 / (a sqrt(2 pi)); it is a
@@ -23,24 +21,11 @@
 
 namespace pts {
 
+// -2 sqrt(2 / pi) / ln 2 and 0.044715 of it
 constexpr float GELU_C = -0x1.26aec2p+1f, GELU_D = -0x1.a5a7d0p-4f;
 
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 
-// exp(x + dx) for x <= 0 and a small dx: t = x / ln 2 rounded, and what that misses of the exponent (ln 2 in two parts).
-__device__ __forceinline__ float exp_of(float x, float dx)
-{
-    const float t = x * 0x1.715476p+0f;
-    const float l = fmaf(0x1.05c61p-29f, t, fmaf(-0x1.62e43p-1f, t, x)) + dx;
-    const float e = __builtin_amdgcn_exp2f(t);
-    return fmaf(e, l, e);
-}
-// 1 / d for d in [1, 2^60]: the hardware's reciprocal, refined once.
-__device__ __forceinline__ float reciprocal(float d)
-{
-    const float r = __builtin_amdgcn_rcpf(d);
-    return fmaf(fmaf(-d, r, 1.0f), r, r);
-}
 // v within [-most, most]; NaN stays.
 __device__ __forceinline__ float within(float v, float most) { return v > most ? most : v < -most ? -most : v; }
 
@@ -58,42 +43,29 @@ __device__ __forceinline__ float normal_poly(float t)
     return fmaf(g, t, 0x1.1df1c6p-3f);
 }
 
-// exp(-z^2 / 2) and Phi(-|z|).
+// exp(-a^2 / 2) and Phi(-a), a >= 0.
 struct Normal {
     float bell, below;
 };
-__device__ __forceinline__ Normal normal(float z)
+__device__ __forceinline__ Normal normal(float a)
 {
-    const float a = fabsf(within(z, 16.0f)); // beyond, both are 0
-    const float h = a * a;
     Normal n;
-    n.bell = exp_of(-0.5f * h, -0.5f * fmaf(a, a, -h));
-    const float t = reciprocal(fmaf(0.35f, a, 1.0f));
+    n.bell = __builtin_amdgcn_exp2f(a * a * -0x1.715476p-1f); // -1 / (2 ln 2)
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.35f, a, 1.0f));
     n.below = n.bell * (normal_poly(t) * t);
     return n;
 }
 
-// The logistic function of u and its complement's product with it: p and p (1 - p), from e = exp(-|u|), since 1 - p is
-// lost in the rounding of a p near 1. du: what u is short of its value.
+// The logistic function p of an argument whose negative over ln 2 is u, and p (1 - p), from 2^-|u|, since 1 - p is lost in
+// the rounding of a p near 1.
 struct Logistic {
     float p, slope;
 };
-__device__ __forceinline__ Logistic logistic(float u, float du)
+__device__ __forceinline__ Logistic logistic(float u)
 {
-    u = within(u, 128.0f); // beyond, e is 0
-    const float e = exp_of(-fabsf(u), u < 0.f ? du : -du);
-    const float r = reciprocal(1.0f + e);
-    return Logistic{u < 0.f ? e * r : r, e * r * r};
-}
-
-// 2 sqrt(2 / pi) (z + 0.044715 z^3), as a rounded value and the rest; beyond |z| = 16 its logistic is 0 or 1.
-__device__ __forceinline__ float tanh_argument(float z, float &rest)
-{
-    const float c = within(z, 16.0f), s = c * c;
-    const float f = fmaf(s, 0x1.2444f2p-4f, 0x1.988454p+0f); // 2 sqrt(2 / pi) (1 + 0.044715 s)
-    const float u = c * f;
-    rest = fmaf(c, f, -u);
-    return u;
+    const float e = __builtin_amdgcn_exp2f(-fabsf(u));
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    return Logistic{u > 0.f ? e * r : r, e * r * r};
 }
 
 template <int ACT> __device__ __forceinline__ float activate(float z)
@@ -102,9 +74,7 @@ template <int ACT> __device__ __forceinline__ float activate(float z)
         return z < 0.f ? 0.f : z;
     if constexpr (ACT == ACT_GELU) {
         const float a = fminf(fabsf(z), 16.0f); // beyond, Phi(-a) is 0
-        const float bell = __builtin_amdgcn_exp2f(a * a * -0x1.715476p-1f); // -1 / (2 ln 2)
-        const float t = __builtin_amdgcn_rcpf(fmaf(0.35f, a, 1.0f));
-        return (z < 0.f ? 0.f : z) - a * (bell * (normal_poly(t) * t));
+        return (z < 0.f ? 0.f : z) - a * normal(a).below;
     }
     if constexpr (ACT == ACT_GELU_TANH) { // z / (1 + 2^(z (c + d z^2))), c = -2 sqrt(2 / pi) / ln 2, d = 0.044715 c
         const float e = __builtin_amdgcn_exp2f(z * fmaf(z * z, GELU_D, GELU_C));
@@ -119,21 +89,20 @@ template <int ACT> __device__ __forceinline__ float activation_slope(float z)
 {
     if constexpr (ACT == ACT_RELU)
         return z > 0.f ? 1.f : 0.f;
-    if constexpr (ACT == ACT_GELU) {
-        const Normal n = normal(z);
+    if constexpr (ACT == ACT_GELU) { // Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi)
         const float c = within(z, 16.0f);
-        return fmaf(c * 0x1.988454p-2f, n.bell, z > 0.f ? 1.0f - n.below : n.below); // Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi)
+        const Normal n = normal(fabsf(c));
+        return fmaf(c * 0x1.988454p-2f, n.bell, z > 0.f ? 1.0f - n.below : n.below);
     }
-    if constexpr (ACT == ACT_GELU_TANH) {
-        float rest;
-        const float u = tanh_argument(z, rest);
-        const Logistic l = logistic(u, rest);
-        const float c = within(z, 16.0f);
-        return fmaf(c * fmaf(c * c, 3.0f * 0x1.2444f2p-4f, 0x1.988454p+0f), l.slope, l.p);
+    if constexpr (ACT == ACT_GELU_TANH) { // p + z p (1 - p) u', u = 2 sqrt(2 / pi) (z + 0.044715 z^3)
+        const float c = within(z, 16.0f), s = c * c;
+        const Logistic l = logistic(c * fmaf(s, GELU_D, GELU_C));
+        return fmaf(c * fmaf(s, 3.0f * 0x1.2444f2p-4f, 0x1.988454p+0f), l.slope, l.p);
     }
     if constexpr (ACT == ACT_SILU) {
-        const Logistic l = logistic(z, 0.f);
-        return fmaf(within(z, 128.0f), l.slope, l.p);
+        const float c = within(z, 128.0f);
+        const Logistic l = logistic(c * -0x1.715476p+0f);
+        return fmaf(c, l.slope, l.p);
     }
     return 1.f;
 }
