@@ -116,3 +116,21 @@ def test_slope_of_every_value(pts, act):
     R.check(db, want[0], off[0] + 2 * R.HALF[F32] * want[0].abs(), act)
     for c in range(8):
         assert torch.equal(dw[:, c], db.bfloat16().float())
+
+
+# The least work for each choice of tiles (256, 128 by four or eight waves, 64), none, some or all of them shared.
+@pytest.mark.parametrize("m,n,k", [(70, 200, 40), (70, 200, 1500), (1777, 2500, 40), (1000, 1300, 8000), (2049, 4100, 2100),
+                                   (1000, 2049, 40), (200, 1777, 8000), (1000, 4100, 2100), (2049, 4100, 40),
+                                   (1777, 3001, 8000), (4100, 5000, 4000)])
+def test_every_choice_of_tiles(pts, m, n, k):
+    """The three ways the operands lie, each with the contraction k: exact on integers, edges followed by NaN."""
+    def take(a, b, seed):
+        return padded(a, b, seed, integers=2, pad=float("nan"))
+    x, w = take(m, k, 1), take(n, k, 2)
+    assert torch.equal(pts.linear(x, w, out_dtype=F32), x.float() @ w.float().t())
+    dy, w, x = take(m, k, 3), take(k, n, 4), take(m, n, 5)
+    dx = pts.linear_backward(dy, x, w, need_dw=False, need_dbias=False).dx
+    assert torch.equal(dx, (dy.float() @ w.float()).bfloat16())
+    dy, x, w = take(k, m, 6), take(k, n, 7), take(m, n, 8)
+    dw = pts.linear_backward(dy, x, w, need_dx=False, need_dbias=False, dw_dtype=F32).dw
+    assert torch.equal(dw, dy.float().t() @ x.float())

@@ -113,7 +113,8 @@ def test_empty(pts):
         assert pts.orthogonalize(torch.empty(shape, device=DEV)).shape == shape
 
 
-@pytest.mark.parametrize("shape", [(1100, 1100), (2300, 700), (5, 520, 1000), (600, 6000)])
+@pytest.mark.parametrize("shape", [(1100, 1100), (2300, 700), (5, 520, 1000), (600, 6000), (8, 1024, 2048), (4100, 1500),
+                                   (1500, 4100), (2304, 2304)])
 def test_larger_tiles(pts, shape):
     x = matrix(shape, 9, torch.bfloat16)
     check(pts.orthogonalize(x), x)
