@@ -83,8 +83,9 @@ int64_t pts_linear_backward_workspace(int64_t m, int64_t n, int64_t k, int32_t a
  *   X = x / (|x|_F + eps)
  *   `steps` times: X = a X + b (X X^T) X + c (X X^T)^2 X
  * that is p(s) = a s + b s^3 + c s^5 of its singular values. out: bf16, rounded
- * from fp32. Up to 64 rows or columns all is fp32. Beyond, the products' operands
- * are fp16 and their sums fp32; X, between the steps, is fp16 and eight bits more.
+ * from fp32. Up to 64 rows or columns X and its products are fp32 (its Gram
+ * matrices fp64). Beyond, the products' operands are fp16 and their sums fp32; X,
+ * between the steps, is fp16 and eight bits more.
  *
  * x: row stride ldx >= cols, matrix i at i * x_stride; out likewise (element
  * aligned; its matrices must not overlap). cols and the smaller of rows and cols

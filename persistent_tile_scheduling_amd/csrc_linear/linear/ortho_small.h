@@ -1,17 +1,28 @@
 // Newton-Schulz steps of matrices whose short side is at most 64 (ortho.h has the
-// formulas): all steps in three launches after the norm's, in fp32.
+// formulas): several steps in three launches.
 //
 // The Gram matrix follows the steps without the matrix: with Q = a + b A + c A A,
 // X' = Q X gives A' = Q A Q, and all of them commute. So one workgroup per matrix
 // runs the chain of 64 x 64 products in LDS and leaves each step's b A + c A A;
-// then every workgroup takes 64 of the long side's vectors through all the steps.
-// Where a step at a time costs three products' launches of 6 us (and the joins of
-// split ones), the chain costs 13 products of 64^3 on one compute unit, 1 us each,
-// whatever the long side: 64 x 2000 100 -> 40 us. Beyond 64 a chain in LDS would
-// grow with the cube of the side and lose.
+// then every workgroup takes 64 of the long side's vectors through these steps,
+// in fp32. Beyond 64 a chain in LDS would grow with the cube of the side and lose.
 //
-// The matrix unit multiplies fp32 here (16 x 16 x 4), so nothing is rounded to
-// fewer bits on the way: A's small eigenvalues grow up to 12-fold a step.
+// What the chain cannot do is see X again. An error of A in a direction of small
+// singular values grows by up to a^2 a step (12-fold by the default), where the
+// error of a Gram matrix made from X stays what it is, and an eigenvalue that has
+// become negative runs away: in fp32 ten steps of a matrix of rank 5 come to 1e23.
+// What makes A unsymmetric grows faster still (28-fold), so every product is made
+// on and above the diagonal and its values written to both sides. And the Gram
+// matrix and the chain are of 64 bits, which leaves the growth 29 bits more, and a
+// chain ends, with X written in fp32 and its Gram matrix made anew, before that is
+// used up (chain_steps): after eight steps by the default. Against 64-bit steps
+// this form is as near as fp32 steps that make A from X each time, for any number
+// of steps and whatever the matrix's condition.
+//
+// Five steps of 16 x 16 take 19 us, of 64 x 2000 57, of 32 matrices of 64 x 500 60
+// (a product's launches for each, and the joins of split ones: 75, 104 and 134; a
+// chain in fp32, which did not hold: 17, 48 and 50). The chain's products on one
+// compute unit, at the matrix unit's rate for 64 bits, bound it.
 #pragma once
 
 #include "linear/ortho.h"
@@ -22,18 +33,26 @@ constexpr int SMALL = 64;          // the longest short side
 constexpr int SMALL_PITCH = 68;    // floats of an LDS row: sixteen rows' 16-byte pieces lie in different banks
 constexpr int SMALL_MATRIX = SMALL * SMALL;
 
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
 struct SmallArgs {
-    NormArgs norm;      // x and its norm
-    float *parts;       // [matrix][chunk][64][64]: Gram matrices of chunks of the long side
+    NormArgs norm;      // x and its norm, or X as the chain before left it
+    double *parts;      // [matrix][chunk][block][lane][4]: Gram matrices of chunks of the long side, 16 x 16 blocks on and
+                        //   above the diagonal as the matrix unit leaves them
     float *polys;       // [matrix][step][64][64]: b A + c A A
+    float *mid;         // X for the next chain, rows x cols each (it may be norm.x), or null: the last steps
     uint16_t *out;
     int64_t ldo, o_batch;
     float a, b, c;
-    int32_t tall, side, lng, chunks, chunk, steps, o_whole; // chunk: vectors each, a multiple of 64
+    int32_t scaled;     // norm.x is X already
+    int32_t tall, side, lng, chunks, chunk, steps; // chunk: vectors each, a multiple of 64; steps: of this chain
 };
 
 __device__ __forceinline__ double small_scale(const SmallArgs &args, int batch)
 {
+    if (args.scaled)
+        return 1.0;
     const int lane = threadIdx.x & 63; // at most 64 blocks
     double sum = lane < args.norm.blocks ? args.norm.sums[(int64_t)batch * args.norm.blocks + lane] : 0.0;
 #pragma unroll
@@ -69,14 +88,59 @@ __device__ __forceinline__ f32x4 small_product(const float *p, const float *q, i
     return acc;
 }
 
-// The Gram matrix of one chunk of the long side: sixteen waves, a 16 x 16 block each.
+// The same in 64 bits, of fp32 or fp64 rows. Its instruction's results of lane l are rows l / 16 + 4 v, so the lane with
+// row i of p is given row 4 (i % 4) + i / 4, which makes them rows 4 (l / 16) + v.
+__device__ __forceinline__ f64x4 four(const float *p)
+{
+    const f32x4 v = *(const f32x4 *)p;
+    return f64x4{(double)v[0], (double)v[1], (double)v[2], (double)v[3]};
+}
+__device__ __forceinline__ f64x4 four(const double *p)
+{
+    const f64x2 lo = *(const f64x2 *)p, hi = *(const f64x2 *)(p + 2);
+    return f64x4{lo[0], lo[1], hi[0], hi[1]};
+}
+template <int PITCH, class T>
+__device__ __forceinline__ f64x4 small_product64(const T *p, const T *q, int blocks, int lane)
+{
+    const int l16 = lane & 15, at = (lane >> 4) * 4;
+    p += ((l16 & 3) * 4 + (l16 >> 2)) * PITCH + at;
+    q += l16 * PITCH + at;
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int k = 0; k < SMALL; k += 16) {
+        if (k >= blocks * 16)
+            break;
+        const f64x4 x = four(p + k), y = four(q + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[e], y[e], acc, 0, 0, 0);
+    }
+    return acc;
+}
+
+// Block `t` on or above the diagonal: (0, 0); (0, 1), (1, 1); (0, 2), ..; how many there are up to a side.
+__device__ __forceinline__ void small_block(int t, int &r, int &c)
+{
+    c = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
+    r = t - c * (c + 1) / 2;
+}
+__host__ __device__ inline int small_blocks(int side)
+{
+    const int n = (side + 15) / 16;
+    return n * (n + 1) / 2;
+}
+
+// The Gram matrix of one chunk of the long side: a wave for each of up to ten blocks.
 __global__ __launch_bounds__(1024) void small_gram_kernel(const SmallArgs args)
 {
     __shared__ __align__(16) float x[SMALL * SMALL_PITCH]; // [element][vector]
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int batch = blockIdx.y, r = wave >> 2, c = wave & 3;
+    const int batch = blockIdx.y, blocks = small_blocks(args.side);
+    int r, c;
+    small_block(wave, r, c);
     const double scale = small_scale(args, batch);
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
     const int64_t first = (int64_t)blockIdx.x * args.chunk;
     for (int64_t j0 = first; j0 < min(first + args.chunk, (int64_t)args.lng); j0 += 64) {
         float v[4];
@@ -92,61 +156,71 @@ __global__ __launch_bounds__(1024) void small_gram_kernel(const SmallArgs args)
             x[i * SMALL_PITCH + j] = v[u];
         }
         barrier_lds();
-        acc = small_product(x + r * 16 * SMALL_PITCH, x + c * 16 * SMALL_PITCH, 4, lane, acc);
+        if (wave < blocks)
+            acc += small_product64<SMALL_PITCH>(x + r * 16 * SMALL_PITCH, x + c * 16 * SMALL_PITCH, 4, lane);
     }
-    float *const part = args.parts + ((int64_t)batch * args.chunks + blockIdx.x) * SMALL_MATRIX;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        part[(r * 16 + (lane >> 4) * 4 + e) * SMALL + c * 16 + (lane & 15)] = acc[e];
+    if (wave >= blocks)
+        return;
+    double *const part = args.parts + ((((int64_t)batch * args.chunks + blockIdx.x) * blocks + wave) * 64 + lane) * 4;
+    *(f64x2 *)part = f64x2{acc[0], acc[1]};
+    *(f64x2 *)(part + 2) = f64x2{acc[2], acc[3]};
 }
 
-// The chain of one matrix: A from the chunks' parts, then for each step b A + c A A, and A' = Q (Q A).
-__global__ __launch_bounds__(1024) void small_chain_kernel(const SmallArgs args)
+// The chain of one matrix: A from the chunks' parts, then for each step b A + c A A, and A' = Q (Q A). A wave has a block
+// on or above the diagonal; a lane's four results are of one column.
+__global__ __launch_bounds__(640) void small_chain_kernel(const SmallArgs args)
 {
-    __shared__ __align__(16) float A[SMALL * SMALL_PITCH], Q[SMALL * SMALL_PITCH], T[SMALL * SMALL_PITCH];
+    constexpr int PITCH = SMALL + 2; // sixteen rows' 16-byte pieces lie in different banks
+    __shared__ __align__(16) double A[SMALL * PITCH], Q[SMALL * PITCH], T[SMALL * PITCH];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int batch = blockIdx.x, r = wave >> 2, c = wave & 3, blocks = (args.side + 15) / 16;
+    const int batch = blockIdx.x, high = (args.side + 15) / 16, blocks = small_blocks(args.side);
+    int r, c;
+    small_block(wave, r, c);
     const int col = c * 16 + (lane & 15), row = r * 16 + (lane >> 4) * 4;
-    const float *const part = args.parts + (int64_t)batch * args.chunks * SMALL_MATRIX;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const bool used = r * 16 < args.side && c * 16 < args.side; // blocks past the side are 0 and stay so
-#pragma unroll 4
-    for (int p = 0; p < args.chunks; ++p)
+    const bool used = wave < blocks;
+    // v to its place and to the reflected one
+    auto put = [&](auto *m, int pitch, const auto &v) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            v[e] += part[p * SMALL_MATRIX + (row + e) * SMALL + col];
-    // a lane's four results are of one column: they go to its row of the (symmetric) matrix
-    const int at = col * SMALL_PITCH + row;
-    *(f32x4 *)(A + at) = *(f32x4 *)v;
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    if (!used) {
-        *(f32x4 *)(Q + at) = zero;
-        *(f32x4 *)(T + at) = zero;
+            if (r < c || row + e <= col)
+                m[(row + e) * pitch + col] = m[col * pitch + row + e] = v[e];
+    };
+    auto product = [&](const double *p, const double *q) {
+        return small_product64<PITCH>(p + r * 16 * PITCH, q + c * 16 * PITCH, high, lane);
+    };
+    if (used) {
+        const double *part = args.parts + (((int64_t)batch * args.chunks * blocks + wave) * 64 + lane) * 4;
+        f64x4 v = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+        for (int p = 0; p < args.chunks; ++p)
+            v += four(part + p * blocks * 256);
+        put(A, PITCH, v);
     }
-    float *poly = args.polys + (int64_t)batch * args.steps * SMALL_MATRIX + row * SMALL + col;
-    auto product = [&](const float *p, const float *q) { return small_product(p + r * 16 * SMALL_PITCH, q + c * 16 * SMALL_PITCH, blocks, lane, zero); };
+    float *poly = args.polys + (int64_t)batch * args.steps * SMALL_MATRIX;
     barrier_lds();
     for (int s = 0; s < args.steps; ++s, poly += SMALL_MATRIX) {
         if (used) {
-            const f32x4 square = product(A, A), mine = *(const f32x4 *)(A + at);
-            f32x4 q;
+            const f64x4 square = product(A, A), mine = four(A + col * PITCH + row);
+            f64x4 q;
+            f32x4 p;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                q[e] = fmaf(args.c, square[e], args.b * mine[e]);
-                poly[e * SMALL] = q[e];
+                q[e] = fma((double)args.c, square[e], (double)args.b * mine[e]);
+                p[e] = (float)q[e]; // X's products are of 32 bits
                 if (row + e == col)
-                    q[e] += args.a;
+                    q[e] += (double)args.a;
             }
-            *(f32x4 *)(Q + at) = q;
+            put(poly, SMALL, p);
+            put(Q, PITCH, q);
         }
         if (s + 1 == args.steps)
             return;
         barrier_lds();
         if (used)
-            *(f32x4 *)(T + at) = product(Q, A);
+            put(T, PITCH, product(Q, A));
         barrier_lds();
         if (used)
-            *(f32x4 *)(A + at) = product(Q, T);
+            put(A, PITCH, product(Q, T));
         barrier_lds();
     }
 }
@@ -211,12 +285,16 @@ __global__ __launch_bounds__(256) void small_update_kernel(const SmallArgs args)
         wave_lds_exchange();
     }
     barrier_lds();
+    const int64_t mid = batch * ((int64_t)args.norm.rows * args.norm.cols);
     uint16_t *const out = args.out + batch * args.o_batch;
     for (int at = tid; at < SMALL * 64; at += 256) {
         const int i = args.tall ? at & 63 : at >> 6, j = args.tall ? at >> 6 : at & 63;
         if (i < args.side && j0 + j < args.lng) {
-            const __bf16 v = (__bf16)x[j * SMALL_PITCH + i];
-            out[args.tall ? (j0 + j) * args.ldo + i : i * args.ldo + j0 + j] = __builtin_bit_cast(uint16_t, v);
+            const float v = x[j * SMALL_PITCH + i];
+            if (args.mid != nullptr)
+                args.mid[mid + (args.tall ? (j0 + j) * args.side + i : (int64_t)i * args.lng + j0 + j)] = v;
+            else
+                out[args.tall ? (j0 + j) * args.ldo + i : i * args.ldo + j0 + j] = __builtin_bit_cast(uint16_t, (__bf16)v);
         }
     }
 }

@@ -39,9 +39,11 @@ Layout layout(int64_t count, int64_t rows, int64_t cols)
     return l;
 }
 
-// The same for short sides of up to 64: the squares' sums, the chunks' Gram matrices, the steps' polynomials.
+// The same for short sides of up to 64: the squares' sums, the chunks' Gram matrices, a chain's polynomials, and, since
+// the coefficients decide how many chains the steps take, X between them.
+constexpr int32_t CHAIN = 16; // the most steps of a chain
 struct SmallLayout {
-    int64_t parts, polys, all;
+    int64_t parts, polys, mid, all;
     int32_t blocks, chunks, chunk;
 };
 SmallLayout small_layout(int64_t count, int64_t rows, int64_t cols, int64_t steps)
@@ -52,8 +54,9 @@ SmallLayout small_layout(int64_t count, int64_t rows, int64_t cols, int64_t step
     l.chunk = (int32_t)(ceil_div(ceil_div(lng, 64), 32) * 64); // at most 32 chunks: one workgroup adds them up
     l.chunks = (int32_t)ceil_div(lng, l.chunk);
     l.parts = round16(count * l.blocks * 8);
-    l.polys = l.parts + count * l.chunks * SMALL_MATRIX * 4;
-    l.all = l.polys + count * steps * SMALL_MATRIX * 4;
+    l.polys = l.parts + count * l.chunks * small_blocks((int)std::min(rows, cols)) * 256 * 8;
+    l.mid = l.polys + count * std::min<int64_t>(steps, CHAIN) * SMALL_MATRIX * 4;
+    l.all = l.mid + (steps > 1 ? round16(count * rows * cols * 4) : 0);
     return l;
 }
 
@@ -92,6 +95,38 @@ double reach(double a, double b, double c, double top)
     return most;
 }
 
+// The largest |c0 + c1 t + c2 t^2| on [0, top].
+double most(double c0, double c1, double c2, double top)
+{
+    auto value = [&](double t) { return std::fabs(c0 + t * (c1 + t * c2)); };
+    const double t = c2 != 0.0 ? -c1 / (2.0 * c2) : 0.0;
+    return std::max({value(0.0), value(top), t > 0.0 && t < top ? value(t) : 0.0});
+}
+
+// How many of `steps` steps one chain may take (at least one), X's singular values being in [0, top]; top then has the
+// bound after them.
+//
+// A step takes an eigenvalue t = s^2 of A to f(t) = t q(t)^2, q(t) = a + b t + c t^2, so an error of A grows by at most
+// the largest |f'| = |q p'|, and comes into X' by the largest |q'| times top: it starts as 2^-50 of A (the rounding of
+// its sums in 64 bits) and is kept below 2^-14 of the result, a sixtieth of its rounding to bf16. X's own rounding in
+// fp32 grows by at most the largest |q|, and the chain does not see it: its square is missing in A. It starts as 2^-22
+// (some steps of fp32) and is kept below 2^-6 of X, so that 2^-12 is missing. By the default coefficients the latter
+// ends a chain, after eight steps with 2^-7.
+int32_t chain_steps(double a, double b, double c, double &top, int32_t steps)
+{
+    double error = 0.0, noise = 0.0;
+    for (int32_t i = 0;; ++i) {
+        const double t = top * top, next = std::max(reach(a, b, c, top), 1e-30);
+        const double q = most(a, b, c, t);
+        error += 0x1p-50 * t;
+        noise = (noise + 0x1p-22 * top) * q;
+        if (i > 0 && (i == std::min(steps, CHAIN) || !(error * most(b, 2.0 * c, 0.0, t) * top <= 0x1p-14 * next) || !(noise <= 0x1p-6 * next)))
+            return i;
+        error *= q * most(a, 3.0 * b, 5.0 * c, t);
+        top = next;
+    }
+}
+
 gemm_status run_small(NormArgs &norm, uint8_t *work, void *out, int64_t ldo, int64_t o_batch, int64_t count, int32_t steps, float a,
                       float b, float c, void *stream)
 {
@@ -99,7 +134,7 @@ gemm_status run_small(NormArgs &norm, uint8_t *work, void *out, int64_t ldo, int
     norm.blocks = l.blocks;
     SmallArgs args{};
     args.norm = norm;
-    args.parts = (float *)(work + l.parts);
+    args.parts = (double *)(work + l.parts);
     args.polys = (float *)(work + l.polys);
     args.out = (uint16_t *)out;
     args.ldo = ldo;
@@ -112,13 +147,24 @@ gemm_status run_small(NormArgs &norm, uint8_t *work, void *out, int64_t ldo, int
     args.lng = std::max(norm.rows, norm.cols);
     args.chunks = l.chunks;
     args.chunk = l.chunk;
-    args.steps = steps;
     gemm_status st;
-    if ((st = launch_grid(&norm_kernel, l.blocks, count, 256, stream, norm)) != GEMM_OK ||
-        (st = launch_grid(&small_gram_kernel, l.chunks, count, 1024, stream, args)) != GEMM_OK ||
-        (st = launch_grid(&small_chain_kernel, count, 1, 1024, stream, args)) != GEMM_OK)
+    if ((st = launch_grid(&norm_kernel, l.blocks, count, 256, stream, norm)) != GEMM_OK)
         return st;
-    return launch_grid(&small_update_kernel, ceil_div(args.lng, 64), count, 256, stream, args);
+    double top = 1.0;
+    for (int32_t left = steps; left > 0; left -= args.steps) {
+        args.steps = chain_steps(a, b, c, top, left);
+        args.mid = args.steps < left ? (float *)(work + l.mid) : nullptr;
+        if ((st = launch_grid(&small_gram_kernel, l.chunks, count, 1024, stream, args)) != GEMM_OK ||
+            (st = launch_grid(&small_chain_kernel, count, 1, 64 * small_blocks(args.side), stream, args)) != GEMM_OK ||
+            (st = launch_grid(&small_update_kernel, ceil_div(args.lng, 64), count, 256, stream, args)) != GEMM_OK)
+            return st;
+        args.norm.x = args.mid;
+        args.norm.ldx = norm.cols;
+        args.norm.x_batch = (int64_t)norm.rows * norm.cols;
+        args.norm.f32 = 1;
+        args.scaled = 1;
+    }
+    return GEMM_OK;
 }
 
 } // namespace

@@ -251,9 +251,9 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     ``x``: (rows, cols), or (count, rows, cols): a stack of matrices, each by
     itself; bf16 or fp32, rows or columns contiguous. ``out``: bf16, of ``x``'s shape,
     written in place when given, must not share memory with ``x`` (not checked).
-    Up to 64 rows or columns all is fp32; beyond, the products are of fp16 operands
-    and the matrix itself has eight bits more. The coefficients must keep the singular values of [0, 1] below 8 (5 steps of the
-    defaults: 1.2).
+    Up to 64 rows or columns all is fp32 or more; beyond, the products are of fp16
+    operands and the matrix itself has eight bits more. The coefficients must keep
+    the singular values of [0, 1] below 8 (the defaults: 1.2).
     """
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or x.dim() not in (2, 3):
         _expect("x", x, _VALUES, (None, None))
