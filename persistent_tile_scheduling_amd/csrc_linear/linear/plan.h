@@ -11,7 +11,7 @@
 namespace pts {
 
 constexpr int64_t UNITS = 256; // compute units of the card: the choice, and with it every bit of a result, depends on sizes alone
-constexpr int64_t MAX_EXTENT = INT32_MAX - 1024; // extents are rounded up to whole tiles in 32 bits
+constexpr int64_t MAX_EXTENT = INT64_C(0x7FFFFC00); // 2^31 - 1024: extents below it are rounded up to whole tiles in 32 bits
 
 struct Split {
     int edge;            // tiles are edge x edge,

@@ -1,0 +1,38 @@
+"""The linear layer's C ABI and binding at their limits, without a GPU: what is refused, and what is not."""
+from __future__ import annotations
+
+import pytest
+
+P = 4096            # a pointer that passes the alignment checks; nothing here reaches a launch
+BIG = 1 << 62
+MOST = 2 ** 31 - 1025   # the largest extent
+
+
+@pytest.fixture(scope="module")
+def pts():
+    import persistent_tile_scheduling_amd as mod
+    return mod
+
+
+def refused(pts, call, status, fragment):
+    with pytest.raises(pts.GemmError) as ei:
+        call()
+    assert ei.value.status == status and fragment in str(ei.value), str(ei.value)
+
+
+LINEAR = dict(x=P, ldx=64, w=P, ldw=64, bias=None, dtype_bias=0, act=0, residual=None, ldr=0, y=P, ldy=40, dtype=0, z=None,
+              ldz=0, m=33, n=40, k=64, work=P, bytes=BIG)
+BACK = dict(dy=P, ld_dy=40, z=P, ldz=40, act=4, x=P, ldx=64, w=P, ldw=64, dx=P, ld_dx=64, dw=P, ld_dw=64, dtype=0, db=P,
+            m=33, n=40, k=64, work=P, bytes=BIG)
+ORTHO = dict(x=P, dtype=0, ldx=64, xs=0, count=1, rows=40, cols=64, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7, out=P,
+             ldo=64, os=0, work=P, bytes=BIG)
+
+
+def test_the_largest_extents(pts):
+    """Extents are below 2^31 - 1024: one less passes their check (and is refused for its pointer here)."""
+    for most, fragment in ((MOST, "x: NULL"), (MOST + 1, "m, n and k")):
+        refused(pts, lambda: pts.pts_linear(*{**LINEAR, "m": most, "x": None}.values(), stream=0), 1, fragment)
+    for most, fragment in ((MOST, "dy: NULL"), (MOST + 1, "m, n and k")):
+        refused(pts, lambda: pts.pts_linear_backward(*{**BACK, "m": most, "dy": None}.values(), stream=0), 1, fragment)
+    for most, fragment in ((MOST, "x: NULL"), (MOST + 1, "count, rows and cols")):
+        refused(pts, lambda: pts.pts_orthogonalize(*{**ORTHO, "rows": most, "x": None}.values(), stream=0), 1, fragment)
