@@ -43,7 +43,7 @@ __global__ __launch_bounds__(16 * HIGH) void slope_kernel(const SlopeArgs args)
     __shared__ __align__(16) float part[HIGH][128 + 4];
     const int tid = threadIdx.x, x = tid & 15, y = tid >> 4;
     const int col = blockIdx.x * 128 + x * 8;
-    const int row0 = blockIdx.y * args.rows, end = min(args.m, row0 + args.rows);
+    const int row0 = blockIdx.y * args.rows, end = row0 + min(args.rows, args.m - row0); // row0 + rows can pass 2^31
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (col < args.n)
         with_activation(args.act, [&](auto act) { slope_rows<decltype(act)::value, HIGH>(args, col, row0 + y, end, sum); });
