@@ -20,8 +20,8 @@
  *
  * workspace: 16-byte aligned device memory of at least as many bytes as the
  *   function with _workspace in its name says for the sizes (may be NULL where
- *   that is 0; a call whose sizes are refused: 0); calls that may overlap need
- *   one each.
+ *   that is 0; sizes that every call refuses: 0); calls that may overlap need one
+ *   each.
  */
 #ifndef PTS_LINEAR_H
 #define PTS_LINEAR_H

@@ -11,6 +11,7 @@ namespace pts {
 
 constexpr int64_t MAX_PITCH = 1 << 22; // elements: 256 rows of them are within 2^31 bytes
 inline bool extent(int64_t v) { return v >= 0 && v < MAX_EXTENT; }
+inline bool operand_width(int64_t v) { return v <= MAX_PITCH - 8; } // some row stride passes check_operand
 // Row stride of the library's own 16-bit matrices: rows start at whole cache lines, since a k tile of a row that starts
 // inside one takes two (dx of 5000 x 7000 x 3000: 204 us, 178 with aligned rows of dz).
 inline int64_t own_pitch(int64_t n) { return (n + 63) / 64 * 64; }

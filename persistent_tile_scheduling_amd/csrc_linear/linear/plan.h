@@ -70,10 +70,11 @@ inline Split choose_split(int64_t m, int64_t n, int64_t k, int64_t batch, bool s
 inline int64_t part_bytes(const Split &s) { return s.rest * s.splits * s.edge * s.edge * (int64_t)sizeof(float); }
 
 // Whether its launches keep within HIP's 2^32 - 1 threads.
+inline bool launchable(const Split &s) { return s.whole + s.rest * s.splits <= (int64_t)UINT32_MAX / (s.edge == 256 || s.wide ? 512 : 256); }
 inline gemm_status check_launches(const Split &s)
 {
     const int64_t grid = s.whole + s.rest * s.splits;
-    if (grid > (int64_t)UINT32_MAX / (s.edge == 256 || s.wide ? 512 : 256))
+    if (!launchable(s))
         return fail(GEMM_ERR_UNSUPPORTED, "%lld workgroups: too large a problem for one launch", (long long)grid);
     return GEMM_OK;
 }

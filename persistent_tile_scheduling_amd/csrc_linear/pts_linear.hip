@@ -68,13 +68,14 @@ extern "C" {
 
 int64_t pts_linear_workspace(int64_t m, int64_t n, int64_t k)
 {
-    if (!extent(m) || !extent(n) || !extent(k) || m == 0 || n == 0)
+    if (!extent(m) || !extent(n) || !extent(k) || !operand_width(k) || m == 0 || n == 0)
         return 0;
     if (m <= FEW_ROWS) {
-        const RowsPlan p = plan_rows(m, n, k);
+        const RowsPlan p = plan_rows(m, n, k); // strips that no launch holds are not split
         return p.splits == 1 ? 0 : p.splits * m * rows_pitch(n) * (int64_t)sizeof(float);
     }
-    return part_bytes(choose_split(m, n, k, 1, false));
+    const Split s = choose_split(m, n, k, 1, false);
+    return launchable(s) ? part_bytes(s) : 0;
 }
 
 gemm_status pts_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *bias, int32_t dtype_bias,

@@ -48,7 +48,7 @@ extern "C" {
 
 int64_t pts_linear_backward_workspace(int64_t m, int64_t n, int64_t k, int32_t activation)
 {
-    if (!extent(m) || !extent(n) || !extent(k) || m == 0 || n == 0)
+    if (!extent(m) || !extent(n) || !extent(k) || !operand_width(n) || m == 0 || n == 0)
         return 0;
     return layout(m, n, k, activation).all;
 }

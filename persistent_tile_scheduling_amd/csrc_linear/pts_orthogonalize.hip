@@ -65,6 +65,11 @@ bool sizes(int64_t count, int64_t rows, int64_t cols)
     // the workspace's bytes and every product of the extents stay in 64 bits
     return extent(count) && extent(rows) && extent(cols) && (count == 0 || rows == 0 || cols == 0 || rows * cols <= (INT64_C(1) << 48) / count);
 }
+bool widths(int64_t rows, int64_t cols) { return cols <= MAX_PITCH - 64 && std::min(rows, cols) <= MAX_PITCH - 64; }
+bool small_launchable(int64_t count, int64_t rows, int64_t cols)
+{
+    return ceil_div(std::max(rows, cols), 64) * count <= (int64_t)UINT32_MAX / 256;
+}
 
 // The largest |c1 t + c2 t^2| on [0, top].
 double largest(double c1, double c2, double top)
@@ -173,11 +178,12 @@ extern "C" {
 
 int64_t pts_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int32_t steps)
 {
-    if (!sizes(count, rows, cols) || count == 0 || rows == 0 || cols == 0 || steps < 1 || steps > 64)
+    if (!sizes(count, rows, cols) || !widths(rows, cols) || count > 65535 || count == 0 || rows == 0 || cols == 0 || steps < 1 || steps > 64)
         return 0;
     if (std::min(rows, cols) <= SMALL)
-        return small_layout(count, rows, cols, steps).all;
-    return layout(count, rows, cols).all;
+        return small_launchable(count, rows, cols) ? small_layout(count, rows, cols, steps).all : 0;
+    const Layout l = layout(count, rows, cols);
+    return launchable(l.gram_split) && launchable(l.square_split) && launchable(l.update_split) ? l.all : 0;
 }
 
 gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64_t x_stride, int64_t count,
@@ -191,7 +197,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         return fail(GEMM_ERR_INVALID_VALUE, "count, rows and cols must be in [0, 2^31 - 1024), count * rows * cols at most 2^48");
     if (count > 65535)
         return fail(GEMM_ERR_UNSUPPORTED, "%lld matrices; at most 65535", (long long)count);
-    if (cols > MAX_PITCH - 64 || std::min(rows, cols) > MAX_PITCH - 64)
+    if (!widths(rows, cols))
         return fail(GEMM_ERR_UNSUPPORTED, "a tile's offsets must fit in 32-bit: at most 2^22 - 64 columns");
     if (steps < 1 || steps > 64)
         return fail(GEMM_ERR_INVALID_VALUE, "steps must be in [1, 64], not %d", steps);
@@ -220,7 +226,7 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
     if (count == 0 || rows == 0 || cols == 0)
         return GEMM_OK;
     const bool small = std::min(rows, cols) <= SMALL;
-    if (small && ceil_div(std::max(rows, cols), 64) * count > (int64_t)UINT32_MAX / 256)
+    if (small && !small_launchable(count, rows, cols))
         return fail(GEMM_ERR_UNSUPPORTED, "%lld x %lld x %lld: too large a problem for one launch", (long long)count, (long long)rows,
                     (long long)cols);
 

@@ -36,3 +36,24 @@ def test_the_largest_extents(pts):
         refused(pts, lambda: pts.pts_linear_backward(*{**BACK, "m": most, "dy": None}.values(), stream=0), 1, fragment)
     for most, fragment in ((MOST, "x: NULL"), (MOST + 1, "count, rows and cols")):
         refused(pts, lambda: pts.pts_orthogonalize(*{**ORTHO, "rows": most, "x": None}.values(), stream=0), 1, fragment)
+
+
+def test_workspaces_of_refused_sizes(pts):
+    """0, and no overflow on the way, wherever no pointers and strides make the sizes' call pass."""
+    wide = 2 ** 22 - 8      # the widest operand
+    assert pts.pts_linear_workspace(40, 300, wide) > 0 and pts.pts_linear_workspace(40, 300, wide + 1) == 0
+    assert pts.pts_linear_workspace(4, 300, wide) > 0 and pts.pts_linear_workspace(4, 300, wide + 1) == 0
+    assert pts.pts_linear_workspace(MOST, MOST, 8) == 0
+    for act in range(5):
+        assert pts.pts_linear_backward_workspace(MOST, MOST, MOST, act) == 0
+        assert pts.pts_linear_backward_workspace(300, wide, 40, act) > 0
+        assert pts.pts_linear_backward_workspace(300, wide + 1, 40, act) == 0
+        assert pts.pts_linear_backward_workspace(300, wide, MOST, act) > 0     # a call for the bias alone does not look at k
+    assert pts.pts_linear_backward_workspace(MOST, 300, 40, 1) > 2 * MOST * 300
+    assert pts.pts_linear_backward_workspace(64, 72, 64, 4) == 64 * 128 * 2     # dz has rows of whole cache lines
+    ortho = pts.pts_orthogonalize_workspace
+    assert ortho(65535, 64, 64, 5) > 0 and ortho(65536, 64, 64, 5) == 0 and ortho(65536, 80, 80, 5) == 0
+    assert ortho(1, 64, 2 ** 22 - 64, 5) > 0 and ortho(1, 64, 2 ** 22 - 63, 5) == 0
+    assert ortho(1, 70, 2 ** 22 - 64, 5) > 0 and ortho(1, 70, 2 ** 22 - 63, 5) == 0 and ortho(1, 2 ** 22 - 63, 70, 5) > 0
+    assert ortho(65535, 64, 2 ** 15, 5) == 0      # too large for one launch
+    assert ortho(MOST, MOST, MOST, 64) == 0 and ortho(1, MOST, 64, 64) > 0
