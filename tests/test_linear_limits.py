@@ -56,4 +56,4 @@ def test_workspaces_of_refused_sizes(pts):
     assert ortho(1, 64, 2 ** 22 - 64, 5) > 0 and ortho(1, 64, 2 ** 22 - 63, 5) == 0
     assert ortho(1, 70, 2 ** 22 - 64, 5) > 0 and ortho(1, 70, 2 ** 22 - 63, 5) == 0 and ortho(1, 2 ** 22 - 63, 70, 5) > 0
     assert ortho(65535, 64, 2 ** 15, 5) == 0      # too large for one launch
-    assert ortho(MOST, MOST, MOST, 64) == 0 and ortho(1, MOST, 64, 64) > 0
+    assert ortho(MOST, MOST, MOST, 64) == 0 and ortho(1, MOST, 64, 64) == 0 and ortho(1, 2 ** 29, 64, 64) > 0
