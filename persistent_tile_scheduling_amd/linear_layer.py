@@ -242,6 +242,20 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
     return LinearGradients(dx, dw, dbias)
 
 
+def _turned(t) -> bool:
+    """Whether a matrix (each of a stack) has contiguous columns and not rows; a single strided row counts as columns."""
+    return t.shape[-1] > 1 and t.stride(-1) != 1 and (t.stride(-2) == 1 or t.shape[-2] == 1)
+
+
+def _apart(t) -> bool:
+    """Whether no two matrices of a stack share an element (one after the other, or between each other's rows)."""
+    if t.dim() < 3 or t.shape[0] < 2 or not t.numel():
+        return True
+    (rows, row), (width, _) = sorted(zip(t.shape[-2:], t.stride()[-2:]), key=lambda d: -d[1])
+    step = t.stride(0)
+    return step >= (rows - 1) * row + width or (step >= width and row >= (t.shape[0] - 1) * step + width)
+
+
 def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """``steps`` Newton-Schulz steps from ``x / (|x|_F + eps)`` towards its orthogonal
@@ -250,6 +264,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
 
     ``x``: (rows, cols), or (count, rows, cols): a stack of matrices, each by
     itself; bf16 or fp32, rows or columns contiguous. ``out``: bf16, of ``x``'s shape,
+    rows or columns contiguous (where not the same as ``x``'s, it takes a copy),
     written in place when given, must not share memory with ``x`` (not checked).
     Up to 64 rows or columns all is fp32 or more; beyond, the products are of fp16
     operands and the matrix itself has eight bits more. The coefficients must keep
@@ -261,8 +276,12 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
         _expect("out", out, (_BF16,), x.shape)
     dev = _device(x, out)
     rows, cols = x.shape[-2:]
-    if cols > 1 and x.stride(-1) != 1 and (x.stride(-2) == 1 or rows == 1):
-        # the factor of a transpose is the transpose of the factor
+    if out is not None and _turned(x) != _turned(out) and rows > 1:
+        _pitch("out", out.transpose(-1, -2) if _turned(out) else out)
+        if not _apart(out):
+            raise ValueError(f"out's matrices overlap (strides {out.stride()})")
+        return out.copy_(orthogonalize(x, steps, coefficients, eps))
+    if _turned(x) or (out is not None and _turned(out)):    # the factor of a transpose is the transpose of the factor
         y = orthogonalize(x.transpose(-1, -2), steps, coefficients, eps, None if out is None else out.transpose(-1, -2))
         return y.transpose(-1, -2) if out is None else out
     if out is None:
