@@ -196,7 +196,7 @@ class LinearGradients(NamedTuple):
     dbias: torch.Tensor | None  # (n) fp32
 
 
-def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.Tensor | None = None,
+def linear_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None, z: torch.Tensor | None = None,
                     activation: str | None = None, dw_dtype=torch.bfloat16, need_dx: bool = True,
                     need_dw: bool = True, need_dbias: bool = True) -> LinearGradients:
     """The gradients of :func:`linear` from ``dy`` (m, n), bf16:
@@ -204,16 +204,21 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
     dz's rows. The residual's gradient is ``dy`` itself.
 
     ``x``, ``w``, ``activation``: as in the forward call; ``z``: (m, n) bf16, its
-    preactivation (with an activation only). All have row strides that are
+    preactivation. ``x`` is for dw only, ``w`` for dx, ``z`` for an activation; they
+    are not looked at otherwise and may be None. All have row strides that are
     multiples of 8 and start 16-byte aligned, as :func:`linear` leaves its results.
     ``dw_dtype``: bf16 or fp32. The products take dz rounded to bf16; dbias (fp32)
     is summed from the unrounded one. A gradient that is not needed is not computed.
     """
-    ld_dy, ldx, ldw = _operand("dy", dy), _operand("x", x), _operand("w", w)
+    ld_dy, xp, wp, ldx, ldw, k = _operand("dy", dy), None, None, 0, 0, 0
     m, n = dy.shape
-    k = w.shape[1]
-    if x.shape != (m, k) or w.shape[0] != n:
-        raise ValueError(f"dy {tuple(dy.shape)}, x {tuple(x.shape)} and w {tuple(w.shape)} do not fit together")
+    if need_dw:
+        ldx, xp, k = _operand("x", x), x.data_ptr(), x.shape[1]
+    if need_dx:
+        ldw, wp, k = _operand("w", w), w.data_ptr(), w.shape[1]
+    if (need_dw and x.shape != (m, k)) or (need_dx and w.shape[0] != n):
+        raise ValueError("dy {}, x {} and w {} do not fit together".format(
+            tuple(dy.shape), *(tuple(t.shape) if need else None for t, need in ((x, need_dw), (w, need_dx)))))
     act, zp, ldz = _activation(activation), None, 0
     if act:
         ldz = _operand("z", z)
@@ -222,7 +227,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
         zp = z.data_ptr()
     if dw_dtype not in _DTYPES:
         raise ValueError(f"dw_dtype must be float32 or bfloat16, not {dw_dtype}")
-    dev, device = _device(dy, x, w, z if act else None), dy.device
+    dev, device = _device(dy, x if need_dw else None, w if need_dx else None, z if act else None), dy.device
     dx = dw = dbias = None
     ld_dx = ld_dw = 0
     if need_dx:
@@ -233,7 +238,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
         dbias = _empty((n,), (1,), dtype=_F32, device=device)
     need = _backward_workspace(m, n, k, act)
     work = _work(need, device)
-    status = _backward(dy.data_ptr(), ld_dy, zp, ldz, act, x.data_ptr(), ldx, w.data_ptr(), ldw,
+    status = _backward(dy.data_ptr(), ld_dy, zp, ldz, act, xp, ldx, wp, ldw,
                        dx.data_ptr() if need_dx else None, ld_dx, dw.data_ptr() if need_dw else None, ld_dw,
                        _DTYPES[dw_dtype], dbias.data_ptr() if need_dbias else None, m, n, k,
                        None if work is None else work.data_ptr(), need, _raw_stream(dev))

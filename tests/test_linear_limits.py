@@ -1,7 +1,10 @@
 """The linear layer's C ABI and binding at their limits, without a GPU: what is refused, and what is not."""
 from __future__ import annotations
 
+import re
+
 import pytest
+import torch
 
 P = 4096            # a pointer that passes the alignment checks; nothing here reaches a launch
 BIG = 1 << 62
@@ -57,3 +60,16 @@ def test_workspaces_of_refused_sizes(pts):
     assert ortho(1, 70, 2 ** 22 - 64, 5) > 0 and ortho(1, 70, 2 ** 22 - 63, 5) == 0 and ortho(1, 2 ** 22 - 63, 70, 5) > 0
     assert ortho(65535, 64, 2 ** 15, 5) == 0      # too large for one launch
     assert ortho(MOST, MOST, MOST, 64) == 0 and ortho(1, MOST, 64, 64) == 0 and ortho(1, 2 ** 29, 64, 64) > 0
+
+
+@pytest.mark.parametrize("change,fragment", [
+    (dict(x=None), "x must be"), (dict(w=None), "w must be"), (dict(w=None, need_dw=False), "w must be"),
+    (dict(x=None, need_dx=False), "x must be"), (dict(x=torch.zeros(5, 8).bfloat16()), "(5, 8)"),
+    (dict(x=torch.zeros(5, 8).bfloat16(), need_dx=False), "w None do not fit"),
+    (dict(w=torch.zeros(9, 8).bfloat16(), need_dw=False), "x None and w (9, 8) do not fit"),
+    (dict(w=torch.zeros(8, 16).bfloat16()), "do not fit"),
+])
+def test_operands_that_are_needed(pts, change, fragment):
+    given = dict(dy=torch.zeros(4, 8).bfloat16(), x=torch.zeros(4, 8).bfloat16(), w=torch.zeros(8, 8).bfloat16())
+    with pytest.raises(ValueError, match=re.escape(fragment)):
+        pts.linear_backward(**{**given, **change})
