@@ -161,19 +161,19 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
                              or (n > 1 and bias.stride(0) != 1)):
         _expect("bias", bias, _VALUES, (n,))
         raise ValueError("bias must be contiguous")
-    dev = _device(x, w, bias, residual, out)
     if out is not None:
         _expect("out", out, _VALUES, (m, n))
-        y, ldy, dtype = out, _pitch("out", out), out.dtype
+        dtype = out.dtype
+    elif out_dtype not in _DTYPES:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, not {out_dtype}")
     else:
-        if out_dtype not in _DTYPES:
-            raise ValueError(f"out_dtype must be float32 or bfloat16, not {out_dtype}")
         dtype = out_dtype
-        y, ldy = _padded(m, n, dtype, x.device)
+    if residual is not None and (not isinstance(residual, torch.Tensor) or residual.dtype is not dtype or residual.shape != (m, n)):
+        _expect("residual", residual, (dtype,), (m, n))
+    dev = _device(x, w, bias, residual, out)
+    y, ldy = _padded(m, n, dtype, x.device) if out is None else (out, _pitch("out", out))
     r = ldr = 0
     if residual is not None:
-        if not isinstance(residual, torch.Tensor) or residual.dtype is not dtype or residual.shape != (m, n):
-            _expect("residual", residual, (dtype,), (m, n))
         r, ldr = residual.data_ptr(), _pitch("residual", residual)
     z, zp, ldz = None, None, 0
     if preactivation:

@@ -73,3 +73,14 @@ def test_operands_that_are_needed(pts, change, fragment):
     given = dict(dy=torch.zeros(4, 8).bfloat16(), x=torch.zeros(4, 8).bfloat16(), w=torch.zeros(8, 8).bfloat16())
     with pytest.raises(ValueError, match=re.escape(fragment)):
         pts.linear_backward(**{**given, **change})
+
+
+@pytest.mark.parametrize("change,fragment", [
+    (dict(residual=3.0), "residual must be bfloat16 of shape (4, 8), not float"), (dict(out=[1]), "out must be"),
+    (dict(residual=torch.zeros(4, 8)), "residual must be bfloat16"), (dict(residual=torch.zeros(4, 9).bfloat16()), "residual must be"),
+    (dict(out=torch.zeros(4, 8).half()), "out must be"), (dict(out=torch.zeros(4, 8), residual=torch.zeros(4, 8).bfloat16()), "residual must be float32"),
+    (dict(bias=1.0), "bias must be"),
+])
+def test_what_is_no_fitting_tensor(pts, change, fragment):
+    with pytest.raises(ValueError, match=re.escape(fragment)):
+        pts.linear(torch.zeros(4, 8).bfloat16(), torch.zeros(8, 8).bfloat16(), **change)
