@@ -279,6 +279,8 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
         _expect("x", x, _VALUES, (None, None))
     if out is not None:
         _expect("out", out, (_BF16,), x.shape)
+    if not isinstance(steps, int) or not 1 <= steps <= 64:
+        raise ValueError(f"steps must be a whole number in [1, 64], not {steps!r}")
     dev = _device(x, out)
     rows, cols = x.shape[-2:]
     if out is not None and _turned(x) != _turned(out) and rows > 1:
@@ -294,7 +296,6 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     ldx, ldo = _pitch("x", x), _pitch("out", out)
     count = x.shape[0] if x.dim() == 3 else 1
     a, b, c = map(float, coefficients)
-    steps = int(steps)
     need = _orthogonalize_workspace(count, rows, cols, steps)
     work = _work(need, x.device)
     status = _orthogonalize(x.data_ptr(), _DTYPES[x.dtype], ldx, x.stride(0) if count > 1 else 0, count, rows, cols,

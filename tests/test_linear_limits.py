@@ -84,3 +84,12 @@ def test_operands_that_are_needed(pts, change, fragment):
 def test_what_is_no_fitting_tensor(pts, change, fragment):
     with pytest.raises(ValueError, match=re.escape(fragment)):
         pts.linear(torch.zeros(4, 8).bfloat16(), torch.zeros(8, 8).bfloat16(), **change)
+
+
+@pytest.mark.parametrize("steps", [5.7, 0, 65, 2 ** 32 + 5, -1, "5", None])
+def test_steps_are_a_whole_number_within_the_range(pts, steps, monkeypatch):
+    """Nothing is cut off or wrapped to a number of steps that is in the range."""
+    from persistent_tile_scheduling_amd import experts
+    monkeypatch.setattr(experts, "_current", lambda: 0)
+    with pytest.raises(ValueError, match="steps must be a whole number"):
+        pts.orthogonalize(torch.zeros(4, 4), steps)
