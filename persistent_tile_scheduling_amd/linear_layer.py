@@ -279,8 +279,9 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
         _expect("x", x, _VALUES, (None, None))
     if out is not None:
         _expect("out", out, (_BF16,), x.shape)
-    if not isinstance(steps, int) or not 1 <= steps <= 64:
+    if steps not in range(1, 65):     # 5.0 and other types' whole numbers are in it
         raise ValueError(f"steps must be a whole number in [1, 64], not {steps!r}")
+    steps = int(steps)
     dev = _device(x, out)
     rows, cols = x.shape[-2:]
     if out is not None and _turned(x) != _turned(out) and rows > 1:

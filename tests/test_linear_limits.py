@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import re
 
+import numpy as np
 import pytest
 import torch
 
@@ -92,4 +93,10 @@ def test_steps_are_a_whole_number_within_the_range(pts, steps, monkeypatch):
     from persistent_tile_scheduling_amd import experts
     monkeypatch.setattr(experts, "_current", lambda: 0)
     with pytest.raises(ValueError, match="steps must be a whole number"):
+        pts.orthogonalize(torch.zeros(4, 4), steps)
+
+
+@pytest.mark.parametrize("steps", [5, 5.0, np.int64(64), np.float32(1), torch.tensor(5)])
+def test_whole_numbers_of_any_type_are_steps(pts, steps):
+    with pytest.raises(ValueError, match="not on the current GPU"):     # the next thing that is checked
         pts.orthogonalize(torch.zeros(4, 4), steps)
