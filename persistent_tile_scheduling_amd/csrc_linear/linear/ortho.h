@@ -180,6 +180,9 @@ template <class F> __device__ __forceinline__ void each_piece(const NormArgs &ar
     }
 }
 
+// 1 / (|x|_F + eps); 0 for a matrix of zeros, since 1 / eps may be infinite (and then 0 / eps is NaN).
+__device__ __forceinline__ double norm_scale(double squares, double eps) { return squares == 0.0 ? 0.0 : 1.0 / (sqrt(squares) + eps); }
+
 // The sum of v over the workgroup's 256 threads, in every thread.
 __device__ __forceinline__ double sum256(double v, double *part)
 {
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(256) void start_kernel(const NormArgs args)
     __shared__ double part[4];
     const double *const sums = args.sums + (int64_t)blockIdx.y * args.blocks;
     const double sum = sum256((int)threadIdx.x < args.blocks ? sums[threadIdx.x] : 0.0, part);
-    const double scale = 1.0 / (sqrt(sum) + args.eps);
+    const double scale = norm_scale(sum, args.eps);
     if (blockIdx.x == 0 && threadIdx.x == 0)
         args.scale[blockIdx.y] = scale;
     each_piece(args, [&](int64_t row, int col, const float(&v)[8]) {

@@ -58,7 +58,7 @@ __device__ __forceinline__ double small_scale(const SmallArgs &args, int batch)
 #pragma unroll
     for (int d = 32; d > 0; d /= 2)
         sum += __shfl_xor(sum, d);
-    return 1.0 / (sqrt(sum) + args.norm.eps);
+    return norm_scale(sum, args.norm.eps);
 }
 
 // Element i of long vector j of x, scaled; 0 outside.

@@ -69,3 +69,12 @@ def test_captured(pts):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, pts.orthogonalize(x, 20))
+
+
+@pytest.mark.parametrize("eps", [5e-324, 1e-310, 1e-7])
+@pytest.mark.parametrize("shape", [(20, 30), (80, 90)])
+def test_zeros_stay_zero_with_any_eps(pts, shape, eps):
+    x = torch.zeros((2, *shape), device="cuda")
+    x[1] = torch.randn(shape, generator=torch.Generator().manual_seed(5)).cuda()
+    y = pts.orthogonalize(x, eps=eps)
+    assert not y[0].any() and torch.isfinite(y[1]).all() and y[1].any()
