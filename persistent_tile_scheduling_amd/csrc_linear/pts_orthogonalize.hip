@@ -71,14 +71,14 @@ bool small_launchable(int64_t count, int64_t rows, int64_t cols)
     return ceil_div(std::max(rows, cols), 64) * count <= (int64_t)UINT32_MAX / 256;
 }
 
-// The largest |c1 t + c2 t^2| on [0, top].
-double largest(double c1, double c2, double top)
+// The largest |c0 + c1 t + c2 t^2| on [0, top].
+double most(double c0, double c1, double c2, double top)
 {
-    double most = std::fabs(c1 * top + c2 * top * top);
-    if (c2 != 0.0 && -c1 / (2.0 * c2) > 0.0 && -c1 / (2.0 * c2) < top)
-        most = std::max(most, std::fabs(c1 * c1 / (4.0 * c2)));
-    return most;
+    auto value = [&](double t) { return std::fabs(c0 + t * (c1 + t * c2)); };
+    const double t = c2 != 0.0 ? -c1 / (2.0 * c2) : 0.0;
+    return std::max({value(0.0), value(top), t > 0.0 && t < top ? value(t) : 0.0});
 }
+
 // The largest |a s + b s^3 + c s^5| on [0, top]: at its end or where a + 3 b t + 5 c t^2 = 0, t = s^2.
 double reach(double a, double b, double c, double top)
 {
@@ -100,12 +100,15 @@ double reach(double a, double b, double c, double top)
     return most;
 }
 
-// The largest |c0 + c1 t + c2 t^2| on [0, top].
-double most(double c0, double c1, double c2, double top)
+// A bound on X's singular values after a step from [0, top], its roundings counted: those of X as an operand, of A and of
+// B, half a step of eps each, come into X' = a X + B X with |B|, with |dB/dA| |A| three times (A is made from two rounded
+// X), and with |B| again. Without them a polynomial that maps [0, top] onto itself but grows beyond would be taken for one
+// that stays (5 s - 20 s^3 + 16 s^5 comes to NaN from six steps on in fp16).
+constexpr double EPS_F16 = 0x1p-11, EPS_F32 = 0x1p-20; // of fp32 some steps: its sums' too
+double bound(double a, double b, double c, double top, double eps)
 {
-    auto value = [&](double t) { return std::fabs(c0 + t * (c1 + t * c2)); };
-    const double t = c2 != 0.0 ? -c1 / (2.0 * c2) : 0.0;
-    return std::max({value(0.0), value(top), t > 0.0 && t < top ? value(t) : 0.0});
+    const double t = top * top;
+    return std::max(reach(a, b, c, top) + eps * top * (2.0 * most(0.0, b, c, t) + 3.0 * t * most(b, 2.0 * c, 0.0, t)), 1e-30);
 }
 
 // How many of `steps` steps one chain may take (at least one), X's singular values being in [0, top]; top then has the
@@ -121,7 +124,7 @@ int32_t chain_steps(double a, double b, double c, double &top, int32_t steps)
 {
     double error = 0.0, noise = 0.0;
     for (int32_t i = 0;; ++i) {
-        const double t = top * top, next = std::max(reach(a, b, c, top), 1e-30);
+        const double t = top * top, next = bound(a, b, c, top, EPS_F32);
         const double q = most(a, b, c, t);
         error += 0x1p-50 * t;
         noise = (noise + 0x1p-22 * top) * q;
@@ -205,11 +208,11 @@ gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64
         return fail(GEMM_ERR_INVALID_VALUE, "eps must be above 0");
     double top = 1.0;
     for (int i = 0; i < steps; ++i) {
-        const double poly = largest(b, c, top * top), next = reach(a, b, c, top);
+        const double poly = most(0.0, b, c, top * top), next = bound(a, b, c, top, std::min(rows, cols) <= SMALL ? EPS_F32 : EPS_F16);
         if (!(poly <= 128.0) || !(next <= 8.0))
             return fail(GEMM_ERR_INVALID_VALUE, "the coefficients take singular values to %g in step %d: beyond fp16's reach",
                         next, i + 1);
-        top = std::max(next, 1e-30);
+        top = next;
     }
     const int size = dtype_x == GEMM_DTYPE_F32 ? 4 : 2;
     if (x_stride < 0 || out_stride < 0 || (count > 1 && (x_stride > INT64_MAX / 16 / count || out_stride > INT64_MAX / 16 / count)))

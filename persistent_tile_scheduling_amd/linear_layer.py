@@ -273,7 +273,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     written in place when given, must not share memory with ``x`` (not checked).
     Up to 64 rows or columns all is fp32 or more; beyond, the products are of fp16
     operands and the matrix itself has eight bits more. The coefficients must keep
-    the singular values of [0, 1] below 8 (the defaults: 1.2).
+    the singular values of [0, 1], with the steps' roundings, below 8 (the defaults: 1.2).
     """
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or x.dim() not in (2, 3):
         _expect("x", x, _VALUES, (None, None))

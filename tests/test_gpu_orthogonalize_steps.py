@@ -78,3 +78,17 @@ def test_zeros_stay_zero_with_any_eps(pts, shape, eps):
     x[1] = torch.randn(shape, generator=torch.Generator().manual_seed(5)).cuda()
     y = pts.orthogonalize(x, eps=eps)
     assert not y[0].any() and torch.isfinite(y[1]).all() and y[1].any()
+
+
+@pytest.mark.parametrize("coefficients,steps,top", [
+    (S.QUINTIC, 64, 1.22), (S.CUBIC, 64, 1.01), ((2.0, -1.5, 0.5), 64, 1.01), ((3.0, -3.2, 1.2), 64, 1.23), ((2.6, -1.0, 0.0), 64, 1.63),
+    ((5.0, -20.0, 16.0), 2, 2.1), ((3.0, -1.0, 0.0), 4, 6.8), ((3.0, -4 / 49, 0.0), 4, 7.7)])
+@pytest.mark.parametrize("shape", [(40, 90), (80, 90), (90, 80), (200, 500)])
+def test_accepted_coefficients_stay_within_reach(pts, shape, coefficients, steps, top):
+    """Singular values at the end of the range (rank 1), inside it, and directions that x does not have."""
+    g = torch.Generator().manual_seed(6)
+    for rank in (1, 3, min(shape)):
+        x = torch.randn((shape[0], rank), generator=g) @ torch.randn((rank, shape[1]), generator=g)
+        y = pts.orthogonalize(x.cuda(), steps, coefficients).double().cpu()
+        assert torch.isfinite(y).all()
+        assert torch.linalg.matrix_norm(y, ord=2) <= top * (1 + S.HALF_BF16), (rank, torch.linalg.matrix_norm(y, ord=2))

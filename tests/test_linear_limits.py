@@ -100,3 +100,26 @@ def test_steps_are_a_whole_number_within_the_range(pts, steps, monkeypatch):
 def test_whole_numbers_of_any_type_are_steps(pts, steps):
     with pytest.raises(ValueError, match="not on the current GPU"):     # the next thing that is checked
         pts.orthogonalize(torch.zeros(4, 4), steps)
+
+
+@pytest.mark.parametrize("rows,coefficients,steps", [
+    # p maps [0, 1] (0 to 2, to 7) onto itself and grows 25-fold (9-fold) beyond: roundings leave it in some steps
+    (80, (5.0, -20.0, 16.0), 3), (40, (5.0, -20.0, 16.0), 5), (80, (3.0, -1.0, 0.0), 5), (40, (3.0, -1.0, 0.0), 7),
+    (80, (3.0, -4 / 49, 0.0), 5), (80, (5.0, -20.0, 16.0), 64), (40, (5.0, -20.0, 16.0), 64),
+])
+def test_coefficients_that_roundings_carry_away(pts, rows, coefficients, steps):
+    a, b, c = coefficients
+    given = {**ORTHO, "rows": rows, "cols": 100, "ldx": 100, "ldo": 100, "a": a, "b": b, "c": c}
+    refused(pts, lambda: pts.pts_orthogonalize(*{**given, "steps": steps}.values(), stream=0), 1, "fp16's reach")
+    # one step fewer is taken (and refused for its pointer here)
+    fewer = steps - 1 if steps < 10 else 2
+    refused(pts, lambda: pts.pts_orthogonalize(*{**given, "steps": fewer, "x": None}.values(), stream=0), 1, "x: NULL")
+
+
+@pytest.mark.parametrize("rows", [40, 80])
+@pytest.mark.parametrize("coefficients", [(3.4445, -4.775, 2.0315), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (2.0, -1.5, 0.5),
+                                          (3.0, -3.2, 1.2), (1.0, 0.0, 0.0), (0.1, 0.0, 0.0), (2.6, -1.0, 0.0)])
+def test_coefficients_that_stay(pts, rows, coefficients):
+    a, b, c = coefficients
+    given = {**ORTHO, "rows": rows, "cols": 100, "ldx": 100, "ldo": 100, "a": a, "b": b, "c": c, "steps": 64, "x": None}
+    refused(pts, lambda: pts.pts_orthogonalize(*given.values(), stream=0), 1, "x: NULL")
