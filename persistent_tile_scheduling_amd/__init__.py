@@ -378,7 +378,7 @@ from .experts import (MoeRouting, PTS_FP8_BLOCK, PTS_MOE_MAX_EXPERTS, PTS_MOE_MA
                       pts_gemm_fp8_experts, pts_moe_combine, pts_moe_combine_backward, pts_moe_route,
                       pts_moe_route_backward, pts_moe_route_workspace, pts_quantize_fp8, quantize_fp8)
 # And the linear layer's, which share the experts' checks.
-from .linear_layer import (LinearGradients, PTS_ACTIVATION_GELU, PTS_ACTIVATION_GELU_TANH, PTS_ACTIVATION_NONE,  # noqa: E402, F401
-                     PTS_ACTIVATION_RELU, PTS_ACTIVATION_SILU, linear, linear_backward, orthogonalize, pts_linear,
-                     pts_linear_backward, pts_linear_backward_workspace, pts_linear_workspace, pts_orthogonalize,
-                     pts_orthogonalize_workspace)
+from .linear_layer import (LinearGradients, PTS_ACTIVATION_GELU, PTS_ACTIVATION_GELU_TANH,  # noqa: E402, F401
+                           PTS_ACTIVATION_NONE, PTS_ACTIVATION_RELU, PTS_ACTIVATION_SILU, linear, linear_backward,
+                           orthogonalize, pts_linear, pts_linear_backward, pts_linear_backward_workspace,
+                           pts_linear_workspace, pts_orthogonalize, pts_orthogonalize_workspace)

@@ -24,7 +24,11 @@ namespace pts {
 
 constexpr float ORTHO_SX = 1024.f; // X entries in fp16, times this (at most 8 before it)
 constexpr float ORTHO_SA = 256.f;  // A and B entries
-constexpr float ORTHO_SR = 512.f;  // half a step of fp16 below 2048 is at most 256 times less than one
+// The rest of an X entry is at most half a step of fp16: 1/2 for entries below 2 (2048 with ORTHO_SX), times this 256, within
+// e4m3's 448. Of larger entries, which only coefficients that take singular values past 2 make, it is cut off there: up to 1/8
+// (entries up to 4) or 9/16 (up to 8) of the half step stay missing. Scales that keep it whole (512, 256 for ORTHO_SX) gave
+// the same errors to two digits in a simulation of such coefficients: the operands' own roundings are larger.
+constexpr float ORTHO_SR = 512.f;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 

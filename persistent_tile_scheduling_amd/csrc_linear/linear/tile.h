@@ -69,7 +69,8 @@ struct TileConfig {
     static_assert(WAVES == 4 || WAVES == 8, "waves");
     static_assert((BM == 64 || BM == 128 || BM == 256) && (BN == 64 || BN == 128 || BN == 256), "tile");
     static_assert(NI <= MI && 16 % OUT_ROWS == 0 && (WTN == 32 || WTN == 64), "wave tile");
-    static_assert(STAGES >= 2 && LDS <= 160 * 1024 && (STAGES - 2) * LOADS <= 63, "ring");
+    // the first wait leaves STAGES - 1 stages' loads of a wave under way: what the counter (6 bits) can be told
+    static_assert(STAGES >= 2 && LDS <= 160 * 1024 && (STAGES - 1) * LOADS <= 63, "ring");
 };
 
 // One operand of a tile: N rows of A (columns of B) by 64 k in a ring stage.

@@ -18,7 +18,7 @@ from typing import NamedTuple
 import torch
 
 from . import GEMM_DTYPE_BF16, GEMM_DTYPE_F32, _check, _lib, _ptr, _stream_handle
-from .experts import _device, _expect, _matrix
+from .experts import _device, _expect
 
 PTS_ACTIVATION_NONE = 0
 PTS_ACTIVATION_RELU = 1
