@@ -70,6 +70,7 @@ int64_t pts_linear_workspace(int64_t m, int64_t n, int64_t k);
  * whose pointer is NULL is not computed; w is needed for dx only, x for dw only.
  * The matrix unit takes dz rounded to bf16 (without an activation it is dy, exact);
  * dbias is summed, in fp32, from the unrounded one. m = 0 gives dw = 0, dbias = 0.
+ * For dbias alone the workspace of PTS_ACTIVATION_NONE is enough.
  */
 gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, int64_t ldz, int32_t activation,
                                 const void *x, int64_t ldx, const void *w, int64_t ldw, void *dx, int64_t ld_dx,

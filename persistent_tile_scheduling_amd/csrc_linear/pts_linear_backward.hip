@@ -74,12 +74,13 @@ gemm_status pts_linear_backward(const void *dy, int64_t ld_dy, const void *z, in
         return st;
     if (!aligned(dbias, 4))
         return fail(GEMM_ERR_INVALID_VALUE, "dbias must be element aligned");
-    if ((st = check_workspace(workspace, workspace_bytes, pts_linear_backward_workspace(m, n, k, activation))) != GEMM_OK)
+    const int32_t dz_of = dx != nullptr || dw != nullptr ? activation : PTS_ACTIVATION_NONE; // the bias's gradient keeps no dz
+    if ((st = check_workspace(workspace, workspace_bytes, pts_linear_backward_workspace(m, n, k, dz_of))) != GEMM_OK)
         return st;
     if (n == 0 && (dx == nullptr || m == 0 || k == 0))
         return GEMM_OK;
 
-    const Layout l = layout(std::max<int64_t>(m, 1), std::max<int64_t>(n, 1), k, activation);
+    const Layout l = layout(std::max<int64_t>(m, 1), std::max<int64_t>(n, 1), k, dz_of);
     if ((dx != nullptr && (st = check_launches(l.dx)) != GEMM_OK) || (dw != nullptr && (st = check_launches(l.dw)) != GEMM_OK))
         return st;
     if (ceil_div(n, 128) * ceil_div(std::max<int64_t>(m, 1), block_rows(m, std::max<int64_t>(n, 1))) > (int64_t)UINT32_MAX / 1024)

@@ -236,7 +236,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | 
         dw, ld_dw = _padded(n, k, dw_dtype, device)
     if need_dbias:
         dbias = _empty((n,), (1,), dtype=_F32, device=device)
-    need = _backward_workspace(m, n, k, act)
+    need = _backward_workspace(m, n, k, act if need_dx or need_dw else PTS_ACTIVATION_NONE)
     work = _work(need, device)
     status = _backward(dy.data_ptr(), ld_dy, zp, ldz, act, xp, ldx, wp, ldw,
                        dx.data_ptr() if need_dx else None, ld_dx, dw.data_ptr() if need_dw else None, ld_dw,
