@@ -93,8 +93,8 @@ int64_t pts_linear_backward_workspace(int64_t m, int64_t n, int64_t k, int32_t a
  * are at most 2^22 - 64, count 65535. 1 <= steps <= 64, eps > 0. The coefficients
  * must keep the singular values, which start within [0, 1], in fp16's reach:
  * GEMM_ERR_INVALID_VALUE if |p|, with the roundings of the steps before it, can
- * come above 8 or |b s^2 + c s^4| above 128 on the way. A matrix with an infinity or a NaN comes out NaN; a matrix of zeros
- * stays zero.
+ * come above 8 or |b s^2 + c s^4| above 128 on the way. A matrix with an infinity
+ * or a NaN comes out NaN; a matrix of zeros stays zero.
  */
 gemm_status pts_orthogonalize(const void *x, int32_t dtype_x, int64_t ldx, int64_t x_stride, int64_t count,
                               int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, double eps,

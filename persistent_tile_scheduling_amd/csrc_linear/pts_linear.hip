@@ -18,9 +18,13 @@ using namespace pts;
 // One row block: strips of 16 columns, sixteen waves (1 x 4096 x 4096 9.3 against
 // 10.0 with eight, 8192 x 8192 28.0 against 31.2), eight where they are split; and
 // strips of 32 where there are many and the rows are short (1 x 8192 x 1024 6.0
-// against 8.9; 8192 x 8192 29.4). Two row blocks: strips of 32, which halve the
-// loads of x (32 x 8192 x 8192: 37 against 51 with 16). With 48 rows the tiles
-// are level or better (48 x 4096 x 4096 15.7 against 18.0).
+// against 8.9; 8192 x 8192 29.4). The border, in calls with weights from memory,
+// 32 against 16: one row of n = 4112 to 14336 at k = 1024 7.3 to 8.7 us against 8.1
+// to 14.3, at 1536 level, at 2048 3 to 10% slower, from 4096 on 3 to 36% slower;
+// twelve rows at 2048 2 to 7% faster, at 4096 and beyond 12% faster to 2% slower.
+// Two row blocks: strips of 32, which halve the loads of x (32 x 8192 x 8192: 37
+// against 51 with 16). With 48 rows the tiles are level or better (48 x 4096 x 4096
+// 15.7 against 18.0).
 constexpr int64_t FEW_ROWS = 32;
 
 struct RowsPlan {
